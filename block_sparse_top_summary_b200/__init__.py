@@ -9,6 +9,10 @@ from .abi import (  # noqa: F401
     decode_width,
     ssa_debug_wait_timeout,
     load_library,
+    ssa_append_paged_q8,
+    ssa_decode_paged_q8,
+    ssa_decode_paged_q8_workspace_size,
+    ssa_page_plan,
     prefill,
     route_width,
     ssa_block_summary,

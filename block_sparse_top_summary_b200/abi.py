@@ -19,6 +19,9 @@ _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "lib", "lib
 SSA_F32 = 0
 SSA_BF16 = 1
 
+SSA_E4M3 = 0
+SSA_I8 = 1
+
 _STATUS = {0: "SSA_OK", 1: "SSA_ERR_INVALID_ARG", 2: "SSA_ERR_UNSUPPORTED", 3: "SSA_ERR_CUDA",
            4: "SSA_ERR_TIMEOUT"}
 
@@ -29,7 +32,8 @@ EXPORTS = ("ssa_status_string", "ssa_version", "ssa_block_summary", "ssa_route",
            "ssa_decode_paged", "ssa_decode_append_paged", "ssa_learned_summary",
            "ssa_route_entmax", "ssa_sparse_attn_fwd_prior", "ssa_route_hierarchical",
            "ssa_decode_per_head", "ssa_decode_per_head_workspace_size",
-           "ssa_sparse_attn_bwd_workspace_size",
+           "ssa_sparse_attn_bwd_workspace_size", "ssa_page_plan", "ssa_append_paged_q8",
+           "ssa_decode_paged_q8_workspace_size", "ssa_decode_paged_q8",
            "ssa_device_error", "ssa_check_device_error", "ssa_debug_wait_timeout")
 
 
@@ -82,6 +86,13 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
     lib.ssa_sparse_attn_fwd_prior.argtypes = [vp, vp, vp, i, vp, vp, vp, i, i, i, i, i, i, i, f,
                                               vp, vp, vp]
     lib.ssa_sparse_attn_uses_tensor_cores.argtypes = [i, i, i, i, i]
+    ll = ctypes.c_longlong
+    lib.ssa_page_plan.argtypes = [vp, vp, vp, i, i, vp, i, i, vp, vp, vp, vp, vp, vp, i, vp]
+    lib.ssa_append_paged_q8.argtypes = [vp, vp, vp, vp, i, vp, vp, vp, vp, vp, vp, i, ll, ll, i, i,
+                                        i, i, i, i, i, vp]
+    lib.ssa_decode_paged_q8_workspace_size.argtypes = [i, i, i, i, i, i, i, ctypes.POINTER(sz)]
+    lib.ssa_decode_paged_q8.argtypes = [vp, i, vp, vp, vp, vp, i, vp, vp, i, i, vp, i, i, i, i, i,
+                                        i, f, vp, vp, vp, sz, vp]
     for name in EXPORTS:
         if name not in ("ssa_status_string", "ssa_version"):
             getattr(lib, name).restype = i
@@ -488,6 +499,194 @@ def ssa_sparse_attn_bwd(Q, K, V, O, dO, lse, idx, cnt, B: int, scale: float | No
         _ptr(dK), _ptr(dV), _ptr(workspace), workspace.numel() * workspace.element_size(),
         _stream(stream)))
     return dQ, dK, dV
+
+
+# ------------------------------------------------- page plan and 8-bit paged cache
+def _on_current_device(tensors: dict):
+    """The library launches on the current device: every tensor has to be there."""
+    dev = torch.cuda.current_device()
+    for n, t in tensors.items():
+        if t is None:
+            continue
+        _need(t, n)
+        if t.get_device() != dev:
+            raise ValueError(f"{n} is on cuda:{t.get_device()}, the current device is cuda:{dev}")
+
+
+def _i32(tensors: dict):
+    for n, t in tensors.items():
+        if t is not None and t.dtype != torch.int32:
+            raise TypeError(f"{n} must be int32, not {t.dtype}")
+
+
+def _shape(t, n: str, want: tuple):
+    if t is not None and tuple(t.shape) != want:
+        raise ValueError(f"{n} must have shape {list(want)}, not {list(t.shape)}")
+
+
+def _launch_on(stream, *own):
+    """The stream's handle; tensors that a call allocates and drops stay alive
+    for the work on it."""
+    if stream is None:
+        return torch.cuda.current_stream().cuda_stream
+    for t in own:
+        if t is not None:
+            t.record_stream(stream)
+    return stream.cuda_stream
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def ssa_page_plan(have, want, page_table, ring, pool, B: int, max_new: int, keep=None, got=None,
+                  cu=None, slots=None, pool_out=None, stream=None):
+    """Pages, slots and lengths of a batch: returns ``(got, cu, slots, pool_out)``.
+
+    ``have``/``want``: ``[batch]`` int32 tokens held and asked for; ``page_table``
+    ``[batch, max_blocks]`` and ``ring`` ``[num_pages]`` are changed in place;
+    ``pool`` ``[2]``: first free entry of the ring and number of free pages.
+    ``keep``: ``[batch]`` leading blocks that are not freed.  ``got=have`` and
+    ``pool_out=pool`` update these in place.
+    """
+    dev = have.device
+    batch, max_blocks = page_table.shape
+    if got is None:
+        got = torch.empty(batch, dtype=torch.int32, device=dev)
+    if cu is None:
+        cu = torch.empty(batch + 1, dtype=torch.int32, device=dev)
+    if slots is None:
+        slots = torch.empty(max_new, dtype=torch.int32, device=dev)
+    if pool_out is None:
+        pool_out = torch.empty(2, dtype=torch.int32, device=dev)
+    args = {"have": have, "want": want, "keep": keep, "page_table": page_table, "ring": ring,
+            "pool": pool, "got": got, "cu": cu, "slots": slots, "pool_out": pool_out}
+    _on_current_device(args)
+    _i32(args)
+    for n, w in (("have", (batch,)), ("want", (batch,)), ("keep", (batch,)), ("got", (batch,)),
+                 ("cu", (batch + 1,)), ("slots", (max_new,)), ("pool", (2,)),
+                 ("pool_out", (2,)), ("ring", (ring.numel(),))):
+        _shape(args[n], n, w)
+    _check("ssa_page_plan", load_library().ssa_page_plan(
+        _addr(have), _addr(want), _addr(keep), batch, B, _addr(page_table), max_blocks,
+        ring.numel(), _addr(ring), _addr(pool), _addr(pool_out), _addr(got), _addr(cu),
+        _addr(slots), max_new, _launch_on(stream)))
+    return got, cu, slots, pool_out
+
+
+def _q8_format(Kp: torch.Tensor, Vp: torch.Tensor) -> int:
+    if Kp.dtype != Vp.dtype:
+        raise TypeError(f"Kp and Vp must have one dtype, not {Kp.dtype} and {Vp.dtype}")
+    if Kp.dtype == torch.float8_e4m3fn:
+        return SSA_E4M3
+    if Kp.dtype == torch.int8:
+        return SSA_I8
+    raise TypeError(f"unsupported cache dtype {Kp.dtype} (float8_e4m3fn or int8)")
+
+
+def _q8_cache(Kp, Ks, Vp, Vs, S, B: int, batch: int, max_blocks: int):
+    """Checks of the cache tensors; returns ``(num_pages, Hkv, d)``."""
+    num_pages, Hkv, _, d = Kp.shape
+    _shape(Kp, "Kp", (num_pages, Hkv, B, d))
+    _shape(Vp, "Vp", (num_pages, Hkv, B, d))
+    _shape(Ks, "Ks", (num_pages, Hkv))
+    _shape(Vs, "Vs", (num_pages, Hkv))
+    _shape(S, "S", (batch, Hkv, max_blocks, d))
+    for n, t in (("Ks", Ks), ("Vs", Vs), ("S", S)):
+        if t is not None and t.dtype != torch.float32:
+            raise TypeError(f"{n} must be float32, not {t.dtype}")
+    return num_pages, Hkv, d
+
+
+def ssa_append_paged_q8(Kp, Ks, Vp, Vs, S, slots, cu, seqlens, k_new, v_new, B: int,
+                        max_blocks: int | None = None, stream=None):
+    """Write the new tokens of a ragged batch into a paged 8-bit cache, in place.
+
+    ``Kp``/``Vp``: ``[num_pages, Hkv, B, d]`` ``float8_e4m3fn`` or ``int8``;
+    ``Ks``/``Vs``: ``[num_pages, Hkv]`` fp32 scales; ``S``: ``[batch, Hkv,
+    max_blocks, d]`` fp32 summaries, or None (then ``max_blocks`` bounds the
+    sequences' blocks); ``slots``, ``cu`` and ``seqlens``: as ``ssa_page_plan``
+    returns them (``seqlens`` is ``got``: the lengths with the new tokens);
+    ``k_new``/``v_new``: ``[T, Hkv, d]`` with ``T = len(slots)``, of equal strides
+    and contiguous in d.
+    """
+    batch = seqlens.shape[0]
+    if S is not None:
+        max_blocks = S.shape[2]
+    elif max_blocks is None:
+        raise ValueError("max_blocks is needed when there are no summaries")
+    _on_current_device({"Kp": Kp, "Ks": Ks, "Vp": Vp, "Vs": Vs, "S": S, "slots": slots, "cu": cu,
+                        "seqlens": seqlens})
+    _i32({"slots": slots, "cu": cu, "seqlens": seqlens})
+    num_pages, Hkv, d = _q8_cache(Kp, Ks, Vp, Vs, S, B, batch, max_blocks)
+    T = slots.numel()
+    _shape(cu, "cu", (batch + 1,))
+    for n, t in (("k_new", k_new), ("v_new", v_new)):
+        if not t.is_cuda or t.get_device() != Kp.get_device():
+            raise ValueError(f"{n} must be on the device of the cache")
+        _shape(t, n, (T, Hkv, d))
+        if t.dtype != k_new.dtype:
+            raise TypeError("k_new and v_new must have one dtype")
+        if T > 0 and (t.stride(2) != 1 or t.stride() != k_new.stride()):
+            raise ValueError("k_new and v_new must have equal strides and be contiguous in d")
+    _check("ssa_append_paged_q8", load_library().ssa_append_paged_q8(
+        _addr(Kp), _addr(Ks), _addr(Vp), _addr(Vs), _q8_format(Kp, Vp), _addr(S), _addr(slots),
+        _addr(cu), _addr(seqlens), _addr(k_new), _addr(v_new), _dtype_code(k_new),
+        k_new.stride(0), k_new.stride(1), batch, T, Hkv, d, B, max_blocks, num_pages,
+        _launch_on(stream)))
+    return Kp, Ks, Vp, Vs, S
+
+
+def ssa_decode_paged_q8_workspace_size(batch: int, Hq: int, Hkv: int, d: int, B: int, topk: int,
+                                       max_blocks: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check("ssa_decode_paged_q8_workspace_size",
+           load_library().ssa_decode_paged_q8_workspace_size(batch, Hq, Hkv, d, B, topk,
+                                                             max_blocks, ctypes.byref(n)))
+    return n.value
+
+
+def ssa_decode_paged_q8(q, Kp, Ks, Vp, Vs, S, page_table, seqlens, B: int, topk: int,
+                        scale: float | None = None, O=None, idx=None, want_idx: bool = True,
+                        workspace=None, stream=None):
+    """One decode step over a paged 8-bit cache: returns ``(O, idx)``.
+
+    The cache as for ``ssa_append_paged_q8``; ``page_table``: ``[batch,
+    max_blocks]`` int32.  A sequence of at most ``topk`` candidate blocks attends
+    all of its cache; ``S`` may be None when ``topk >= max_blocks - 2``.
+    """
+    batch, Hq, d = q.shape
+    max_blocks = page_table.shape[1]
+    num_pages, Hkv, _ = _q8_cache(Kp, Ks, Vp, Vs, S, B, batch, max_blocks)
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    if O is None:
+        O = torch.empty_like(q, memory_format=torch.contiguous_format)
+    width = min(topk, max_blocks) + 2
+    if idx is None and want_idx:
+        idx = torch.empty(batch, Hkv, width, dtype=torch.int32, device=q.device)
+    own = None
+    if workspace is None:
+        own = workspace = torch.empty(
+            ssa_decode_paged_q8_workspace_size(batch, Hq, Hkv, d, B, topk, max_blocks),
+            dtype=torch.uint8, device=q.device)
+    _on_current_device({"q": q, "Kp": Kp, "Ks": Ks, "Vp": Vp, "Vs": Vs, "S": S, "O": O,
+                        "page_table": page_table, "seqlens": seqlens, "idx": idx,
+                        "workspace": workspace})
+    _i32({"page_table": page_table, "seqlens": seqlens, "idx": idx})
+    _shape(Kp, "Kp", (num_pages, Hkv, B, d))
+    _shape(page_table, "page_table", (batch, max_blocks))
+    _shape(seqlens, "seqlens", (batch,))
+    _shape(idx, "idx", (batch, Hkv, width))
+    _shape(O, "O", (batch, Hq, d))
+    if O.dtype != q.dtype:
+        raise TypeError(f"O must be {q.dtype}, not {O.dtype}")
+    _check("ssa_decode_paged_q8", load_library().ssa_decode_paged_q8(
+        _addr(q), _dtype_code(q), _addr(Kp), _addr(Ks), _addr(Vp), _addr(Vs), _q8_format(Kp, Vp),
+        _addr(S), _addr(page_table), max_blocks, num_pages, _addr(seqlens), batch, Hq, Hkv, d, B,
+        topk, scale, _addr(O), _addr(idx), _addr(workspace),
+        workspace.numel() * workspace.element_size(), _launch_on(stream, own)))
+    return O, idx
 
 
 # ------------------------------------------------------------- test hooks

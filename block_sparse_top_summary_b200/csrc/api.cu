@@ -19,6 +19,19 @@ ssa_status check_dims(int d, int B, ssa_dtype dt) {
   return SSA_OK;
 }
 
+// Checks shared by the calls on the 8-bit paged cache.
+ssa_status check_q8(int d, int B, ssa_qformat fmt, ssa_dtype dt, int Hkv, int max_blocks,
+                    int num_pages) {
+  const ssa_status st = check_dims(d, B, dt);
+  if (st != SSA_OK) return st;
+  if (fmt != SSA_E4M3 && fmt != SSA_I8) return SSA_ERR_INVALID_ARG;
+  if (Hkv <= 0 || max_blocks <= 0 || num_pages <= 0) return SSA_ERR_INVALID_ARG;
+  if ((long long)max_blocks * B > 0x7fffffffLL || (long long)num_pages * B > 0x7fffffffLL ||
+      (long long)num_pages * Hkv > 0x7fffffffLL)
+    return SSA_ERR_UNSUPPORTED;
+  return SSA_OK;
+}
+
 ssa_status from_cuda(cudaError_t e) { return e == cudaSuccess ? SSA_OK : SSA_ERR_CUDA; }
 
 // Result word of ssa_check_device_error (one per device).
@@ -56,7 +69,7 @@ const char* ssa_status_string(int status) {
   }
 }
 
-int ssa_version(void) { return 204; }
+int ssa_version(void) { return 205; }
 
 ssa_status ssa_block_summary(const void* K, ssa_dtype dtype, int batch, int Hkv, int N, int d,
                              int B, float* S, ssa_stream stream) {
@@ -393,6 +406,98 @@ ssa_status ssa_decode_append(void* Kc, void* Vc, ssa_dtype dtype, float* S, int3
     return SSA_ERR_INVALID_ARG;
   return from_cuda(ssa::launch_decode_append(Kc, Vc, dtype, S, seqlens, k_new, v_new, batch, Hkv,
                                              Lmax, d, B, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+ssa_status ssa_page_plan(const int32_t* have, const int32_t* want, const int32_t* keep, int batch,
+                         int B, int32_t* page_table, int max_blocks, int num_pages, int32_t* ring,
+                         const int32_t* pool, int32_t* pool_out, int32_t* got, int32_t* cu,
+                         int32_t* slots, int max_new, ssa_stream stream) {
+  if (batch <= 0 || B <= 0 || max_blocks <= 0 || num_pages <= 0 || max_new < 0)
+    return SSA_ERR_INVALID_ARG;
+  if (B % 16 != 0 || B > 128 || batch > ssa::kPlanMaxBatch) return SSA_ERR_UNSUPPORTED;
+  if ((long long)max_blocks * B > 0x7fffffffLL || (long long)num_pages * B > 0x7fffffffLL)
+    return SSA_ERR_UNSUPPORTED;
+  if (have == nullptr || want == nullptr || page_table == nullptr || ring == nullptr ||
+      pool == nullptr || pool_out == nullptr || got == nullptr || cu == nullptr ||
+      (max_new > 0 && slots == nullptr))
+    return SSA_ERR_INVALID_ARG;
+  if (!aligned16(have) || !aligned16(want) || !aligned16(keep) || !aligned16(page_table) ||
+      !aligned16(ring) || !aligned16(pool) || !aligned16(pool_out) || !aligned16(got) ||
+      !aligned16(cu) || !aligned16(slots))
+    return SSA_ERR_INVALID_ARG;
+  return from_cuda(ssa::launch_page_plan(have, want, keep, batch, B, page_table, max_blocks,
+                                         num_pages, ring, pool, pool_out, got, cu, slots, max_new,
+                                         reinterpret_cast<cudaStream_t>(stream)));
+}
+
+ssa_status ssa_append_paged_q8(void* Kp, float* Ks, void* Vp, float* Vs, ssa_qformat fmt, float* S,
+                               const int32_t* slots, const int32_t* cu, const int32_t* seqlens,
+                               const void* k_new, const void* v_new, ssa_dtype dtype,
+                               long long tok_stride, long long head_stride, int batch, int max_new,
+                               int Hkv, int d, int B, int max_blocks, int num_pages,
+                               ssa_stream stream) {
+  ssa_status st = check_q8(d, B, fmt, dtype, Hkv, max_blocks, num_pages);
+  if (st != SSA_OK) return st;
+  if (batch <= 0 || max_new < 0) return SSA_ERR_INVALID_ARG;
+  if (max_new == 0) return SSA_OK;
+  if (max_new / B + 2LL * batch > 0x7fffffffLL || 2 * Hkv > 65535) return SSA_ERR_UNSUPPORTED;
+  if (Kp == nullptr || Ks == nullptr || Vp == nullptr || Vs == nullptr || slots == nullptr ||
+      cu == nullptr || seqlens == nullptr || k_new == nullptr || v_new == nullptr)
+    return SSA_ERR_INVALID_ARG;
+  if (!aligned16(Kp) || !aligned16(Ks) || !aligned16(Vp) || !aligned16(Vs) || !aligned16(S) ||
+      !aligned16(slots) || !aligned16(cu) || !aligned16(seqlens) || !aligned16(k_new) ||
+      !aligned16(v_new))
+    return SSA_ERR_INVALID_ARG;
+  const int epc = dtype == SSA_BF16 ? 8 : 4;  // elements of 16 bytes
+  if (tok_stride <= 0 || head_stride <= 0 || tok_stride % epc != 0 || head_stride % epc != 0)
+    return SSA_ERR_INVALID_ARG;
+  return from_cuda(ssa::launch_append_q8(Kp, Ks, Vp, Vs, fmt, S, slots, cu, seqlens, k_new, v_new,
+                                         dtype, tok_stride, head_stride, batch, max_new, Hkv, d, B,
+                                         max_blocks, num_pages,
+                                         reinterpret_cast<cudaStream_t>(stream)));
+}
+
+ssa_status ssa_decode_paged_q8_workspace_size(int batch, int Hq, int Hkv, int d, int B, int topk,
+                                              int max_blocks, size_t* bytes) {
+  if (bytes == nullptr) return SSA_ERR_INVALID_ARG;
+  ssa_status st = check_q8(d, B, SSA_E4M3, SSA_BF16, Hkv, max_blocks, 1);
+  if (st != SSA_OK) return st;
+  if (batch <= 0 || Hq <= 0 || topk < 0 || Hq % Hkv != 0) return SSA_ERR_INVALID_ARG;
+  *bytes = ssa::plan_q8(batch, Hq, Hkv, d, topk, max_blocks).bytes;
+  return SSA_OK;
+}
+
+ssa_status ssa_decode_paged_q8(const void* q, ssa_dtype dtype, const void* Kp, const float* Ks,
+                               const void* Vp, const float* Vs, ssa_qformat fmt, const float* S,
+                               const int32_t* page_table, int max_blocks, int num_pages,
+                               const int32_t* seqlens, int batch, int Hq, int Hkv, int d, int B,
+                               int topk, float scale, void* O, int32_t* idx, void* workspace,
+                               size_t ws_bytes, ssa_stream stream) {
+  ssa_status st = check_q8(d, B, fmt, dtype, Hkv, max_blocks, num_pages);
+  if (st != SSA_OK) return st;
+  if (batch <= 0 || Hq <= 0 || topk < 0 || Hq % Hkv != 0) return SSA_ERR_INVALID_ARG;
+  if (Hq / Hkv > 8) return SSA_ERR_UNSUPPORTED;
+  if (max_blocks > 16384) return SSA_ERR_UNSUPPORTED;
+  // the 16-key slices of the whole batch are counted in 32 bits
+  if ((long long)batch * max_blocks * (B / 16) > 0x7fffffffLL ||
+      (long long)batch * Hkv > 0x7ffffffeLL)
+    return SSA_ERR_UNSUPPORTED;
+  if (!(scale > 0.f)) return SSA_ERR_INVALID_ARG;
+  if (q == nullptr || Kp == nullptr || Ks == nullptr || Vp == nullptr || Vs == nullptr ||
+      page_table == nullptr || seqlens == nullptr || O == nullptr || workspace == nullptr)
+    return SSA_ERR_INVALID_ARG;
+  if (S == nullptr && topk < max_blocks - 2) return SSA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(Kp) || !aligned16(Ks) || !aligned16(Vp) || !aligned16(Vs) ||
+      !aligned16(S) || !aligned16(page_table) || !aligned16(seqlens) || !aligned16(O) ||
+      !aligned16(idx))
+    return SSA_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return SSA_ERR_INVALID_ARG;
+  const ssa::Q8Plan p = ssa::plan_q8(batch, Hq, Hkv, d, topk, max_blocks);
+  if (ws_bytes < p.bytes) return SSA_ERR_INVALID_ARG;
+  return from_cuda(ssa::launch_decode_q8(p, q, Kp, Ks, Vp, Vs, fmt, dtype, S, page_table,
+                                         max_blocks, num_pages, seqlens, batch, Hq, Hkv, d, B,
+                                         scale, O, idx, workspace,
+                                         reinterpret_cast<cudaStream_t>(stream)));
 }
 
 ssa_status ssa_device_error(int* code) {

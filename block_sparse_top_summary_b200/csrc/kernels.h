@@ -115,6 +115,33 @@ cudaError_t launch_decode_append(void* Kc, void* Vc, ssa_dtype dt, float* S, int
                                  const void* k_new, const void* v_new, int batch, int Hkv,
                                  int Lmax, int d, int B, cudaStream_t st, CacheMap pm = CacheMap{});
 
+// Pages, slots and lengths of a batch (ssa_page_plan).
+constexpr int kPlanMaxBatch = 8192;
+cudaError_t launch_page_plan(const int32_t* have, const int32_t* want, const int32_t* keep,
+                             int batch, int B, int32_t* table, int max_blocks, int num_pages,
+                             int32_t* ring, const int32_t* pool, int32_t* pool_out, int32_t* got,
+                             int32_t* cu, int32_t* slots, int max_new, cudaStream_t st);
+
+// The 8-bit paged cache (ssa_append_paged_q8, ssa_decode_paged_q8).
+cudaError_t launch_append_q8(void* Kp, float* Ks, void* Vp, float* Vs, ssa_qformat fmt, float* S,
+                             const int32_t* slots, const int32_t* cu, const int32_t* seqlens,
+                             const void* kn, const void* vn, ssa_dtype dt, long long tok_stride,
+                             long long head_stride, int batch, int T_max, int Hkv, int d, int B,
+                             int max_blocks, int num_pages, cudaStream_t st);
+
+struct Q8Plan {
+  int kk;     // effective top-k: min(topk, max_blocks)
+  int width;  // idx row width: kk + 2
+  // scratch: block lists (from 0), slices before each sequence, arrivals, partial records
+  size_t off_off, off_ctr, off_part, bytes;
+};
+Q8Plan plan_q8(int batch, int Hq, int Hkv, int d, int topk, int max_blocks);
+cudaError_t launch_decode_q8(const Q8Plan& p, const void* q, const void* Kp, const float* Ks,
+                             const void* Vp, const float* Vs, ssa_qformat fmt, ssa_dtype dt,
+                             const float* S, const int32_t* table, int max_blocks, int num_pages,
+                             const int32_t* seqlens, int batch, int Hq, int Hkv, int d, int B,
+                             float scale, void* O, int32_t* idx_out, void* ws, cudaStream_t st);
+
 // Two-level routing: segments of M complete blocks, then blocks.
 cudaError_t launch_hier_route(const void* Q, ssa_dtype dt, const float* S, int batch, int Hq,
                               int Hkv, int N, int d, int B, int M, int k_seg, int k_blk,

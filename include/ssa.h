@@ -49,6 +49,12 @@ typedef enum {
 
 typedef enum { SSA_F32 = 0, SSA_BF16 = 1 } ssa_dtype;
 
+/* Codes of the 8-bit paged cache (ssa_append_paged_q8). */
+typedef enum {
+  SSA_E4M3 = 0, /* 8-bit floats, 4 exponent and 3 fraction bits, largest 448 */
+  SSA_I8 = 1    /* signed whole numbers, -127 .. 127 */
+} ssa_qformat;
+
 /* Opaque CUDA stream handle; binary-compatible with cudaStream_t. */
 typedef struct CUstream_st* ssa_stream;
 
@@ -63,7 +69,8 @@ const char* ssa_status_string(int status);
  * ssa_sparse_attn_fwd_prior); 2.03 the routing variants (ssa_route_hierarchical,
  * ssa_decode_per_head, ssa_decode_per_head_workspace_size); 2.04 the backward
  * takes a sized workspace (ssa_sparse_attn_bwd_workspace_size) in place of
- * its delta scratch. */
+ * its delta scratch; 2.05 the page plan (ssa_page_plan) and the 8-bit paged
+ * cache (ssa_append_paged_q8, ssa_decode_paged_q8). */
 int ssa_version(void);
 
 /*
@@ -400,6 +407,110 @@ ssa_status ssa_decode_append_paged(void* Kp, void* Vp, ssa_dtype dtype, float* S
                                    const int32_t* page_table, int max_blocks, int num_pages,
                                    int32_t* seqlens, const void* k_new, const void* v_new,
                                    int batch, int Hkv, int d, int B, ssa_stream stream);
+
+/*
+ * Pages, slots and lengths of a batch of requests, on the GPU: the bookkeeping
+ * of a paged cache (the layout of ssa_decode_paged) without a host round trip.
+ * The pages have no counterpart: this is a library convenience.
+ *
+ * Row b holds have[b] tokens in the pages page_table[b, 0 .. ceil(have / B) - 1]
+ * and asks for want[b].  Free pages are a ring: entry (pool[0] + i) % num_pages of
+ * `ring` is the i-th free page, i < pool[1].
+ * - want > have: the row needs n = want - have token slots and the pages
+ *   missing to ceil(want / B).  Rows are served in order: it is granted when
+ *   the tokens asked for by rows 0 .. b come to at most max_new and, if it needs
+ *   a page, the pages asked for by rows 0 .. b to at most pool[1].  Its new
+ *   blocks take the next free pages, in block order.
+ * - want < have (a finished or rolled-back request): granted; the blocks from
+ *   max(ceil(want / B), keep[b]) on go behind the free pages, in order of (row,
+ *   block), and are free from the next call on.  keep (NULL: 0) is the number
+ *   of leading blocks that another row shares and owns (a common prefix): they
+ *   leave the row without becoming free.
+ * - want = have: nothing changes.  have or want outside [0, max_blocks * B]:
+ *   refused, counted as 0 tokens and 0 pages.
+ * Written: got[b] = want[b] where granted, else have[b]; cu[0 .. batch], the sums
+ * of n over the rows before each, at most max_new; slots[0 .. max_new - 1]: for
+ * token i of the rows laid end to end (row b's from cu[b] on), page * B + row in
+ * page, and -1 for the tokens of a row that was refused and behind the last
+ * token; pool_out = {head, count}; the granted rows' new entries of page_table
+ * and the returned pages' entries of ring.  Entries of page_table behind a row's
+ * blocks keep what they held; a returned page beyond what the ring can hold
+ * (a page that was free already) is dropped.
+ * All int32: have, want, keep, got: [batch]; page_table: [batch, max_blocks];
+ * ring: [num_pages]; pool, pool_out: [2]; cu: [batch + 1]; slots: [max_new].
+ * got may be have, and pool_out may be pool; nothing else may overlap.
+ * slots may be NULL when max_new is 0.  Supported: B a multiple of 16 in
+ * [16, 128]; batch <= 8192; max_blocks * B and num_pages * B below 2^31.
+ * Calls on one table or ring must not overlap on the device.
+ */
+ssa_status ssa_page_plan(const int32_t* have, const int32_t* want, const int32_t* keep, int batch,
+                         int B, int32_t* page_table, int max_blocks, int num_pages, int32_t* ring,
+                         const int32_t* pool, int32_t* pool_out, int32_t* got, int32_t* cu,
+                         int32_t* slots, int max_new, ssa_stream stream);
+
+/*
+ * New tokens of a ragged batch into a paged cache of 8-bit codes.
+ *
+ * Kp, Vp: page pools [num_pages, Hkv, B, d] of one-byte codes of format `fmt`;
+ * Ks, Vs: [num_pages, Hkv] fp32, the scale of a page and KV head, a power of
+ * two.  An element stands for code * scale.  QMAX = 448 (SSA_E4M3) or 127
+ * (SSA_I8).
+ *
+ * seqlens: [batch], each sequence's length with its new tokens; cu: [batch + 1],
+ * the new tokens' prefix sums; slots: [max_new], the place of each (got, cu and
+ * slots of ssa_page_plan).  Token cu[b] + i goes to position seqlens[b] - n + i,
+ * n = cu[b + 1] - cu[b].  A sequence's tokens of one block are written together,
+ * and only if the first of them has the slot page * B + position % B of some
+ * page; they then go to that page.  A slot of -1 leaves the block as it was.
+ * For a page and head that receives rows [r0, r1):
+ *   scale = max(old scale if r0 > 0, the least 2^e with e >= -126 and
+ *           |x| <= QMAX 2^e for the new rows' elements x);
+ *   code  = x / scale rounded to the nearest code, ties to even;
+ *   the codes of rows below r0 become code * old scale / scale, rounded
+ *   likewise, when the scale grows; rows from r1 on are left as they were.
+ * A NaN or an infinity among the new rows makes the scale NaN, and so every
+ * attention that reads the block, until row 0 of the page is written again.
+ * When r1 = B the block is complete, and its summary becomes the mean of what
+ * its B keys stand for: S[b, g, j, :].  S: [batch, Hkv, max_blocks, d] fp32, or
+ * NULL for none (the cache is then read whole).
+ *
+ * k_new, v_new: max_new tokens by Hkv heads by d of `dtype`, element (i, g, c)
+ * at i * tok_stride + g * head_stride + c (strides in elements, positive and
+ * multiples of 16 bytes), so that the K of a one-sequence prefill [1, Hkv, N, d]
+ * is taken as it is (strides d and N d).
+ * No two sequences may write one page in one call, and calls on one cache must
+ * not overlap on the device.
+ */
+ssa_status ssa_append_paged_q8(void* Kp, float* Ks, void* Vp, float* Vs, ssa_qformat fmt, float* S,
+                               const int32_t* slots, const int32_t* cu, const int32_t* seqlens,
+                               const void* k_new, const void* v_new, ssa_dtype dtype,
+                               long long tok_stride, long long head_stride, int batch, int max_new,
+                               int Hkv, int d, int B, int max_blocks, int num_pages,
+                               ssa_stream stream);
+
+/*
+ * One decode step over the 8-bit paged cache: ssa_decode_paged with K and V the
+ * values that the codes stand for.  q, O: [batch, Hq, d] of `dtype`; sums and
+ * softmax in fp32, q and P as sums of two f16 (22 bits) on the tensor cores.
+ *
+ * A sequence with at most topk candidate blocks attends its whole cache and its
+ * summaries are not read; S may be NULL when topk >= max_blocks - 2, which is
+ * attention over the whole cache for every sequence.
+ * seqlens, page_table, idx: as for ssa_decode_paged (a length outside
+ * [1, max_blocks * B] writes zeros, and -1 to its idx rows).
+ * workspace: >= ssa_decode_paged_q8_workspace_size(...) bytes, 256-byte aligned,
+ * contents on entry ignored; calls that share one must not overlap on the
+ * device.  Hq / Hkv <= 8; max_blocks <= 16384.
+ */
+ssa_status ssa_decode_paged_q8_workspace_size(int batch, int Hq, int Hkv, int d, int B, int topk,
+                                              int max_blocks, size_t* bytes);
+
+ssa_status ssa_decode_paged_q8(const void* q, ssa_dtype dtype, const void* Kp, const float* Ks,
+                               const void* Vp, const float* Vs, ssa_qformat fmt, const float* S,
+                               const int32_t* page_table, int max_blocks, int num_pages,
+                               const int32_t* seqlens, int batch, int Hq, int Hkv, int d, int B,
+                               int topk, float scale, void* O, int32_t* idx, void* workspace,
+                               size_t ws_bytes, ssa_stream stream);
 
 /*
  * Largest scratch area ssa_decode_noalloc can use (40 MiB).

@@ -33,3 +33,12 @@ from .paged_oracle import (  # noqa: F401
     decode_paged,
     gather_pages,
 )
+from .q8_oracle import (  # noqa: F401
+    QMAX,
+    append_paged_q8,
+    decode_paged_q8,
+    nearest_code,
+    page_plan,
+    q8_scale,
+    q8_values,
+)
