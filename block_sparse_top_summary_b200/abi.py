@@ -9,6 +9,7 @@ allocates nothing).  No step of the method runs here.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 
@@ -502,41 +503,39 @@ def ssa_sparse_attn_bwd(Q, K, V, O, dO, lse, idx, cnt, B: int, scale: float | No
 
 
 # ------------------------------------------------- page plan and 8-bit paged cache
-def _on_current_device(tensors: dict):
-    """The library launches on the current device: every tensor has to be there."""
-    dev = torch.cuda.current_device()
-    for n, t in tensors.items():
-        if t is None:
-            continue
+# A serving step makes these calls back to back and their kernels take a few
+# microseconds, so the checks are one expression a tensor, and the current
+# device and stream are read without building torch's Python objects for them.
+_device = torch._C._cuda_getDevice
+_current_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _arg(n: str, t: torch.Tensor, dtype: torch.dtype, shape: tuple, dev: int) -> int:
+    """The address of an argument that has this type and shape, is contiguous and
+    on the current device (the one the library launches on)."""
+    if (t.dtype is not dtype or t.shape != shape or t.get_device() != dev
+            or not t.is_contiguous()):
         _need(t, n)
-        if t.get_device() != dev:
-            raise ValueError(f"{n} is on cuda:{t.get_device()}, the current device is cuda:{dev}")
+        if t.dtype is not dtype:
+            raise TypeError(f"{n} must be {dtype}, not {t.dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{n} must have shape {list(shape)}, not {list(t.shape)}")
+        raise ValueError(f"{n} is on cuda:{t.get_device()}, the current device is cuda:{dev}")
+    return t.data_ptr()
 
 
-def _i32(tensors: dict):
-    for n, t in tensors.items():
-        if t is not None and t.dtype != torch.int32:
-            raise TypeError(f"{n} must be int32, not {t.dtype}")
-
-
-def _shape(t, n: str, want: tuple):
-    if t is not None and tuple(t.shape) != want:
-        raise ValueError(f"{n} must have shape {list(want)}, not {list(t.shape)}")
-
-
-def _launch_on(stream, *own):
-    """The stream's handle; tensors that a call allocates and drops stay alive
-    for the work on it."""
+def _launch_on(stream, dev: int, *own):
+    """The stream's handle; tensors that a call allocates stay alive for the work
+    on a stream that is not the one they were allocated on."""
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream(dev)
+    if stream.device_index != dev:
+        raise ValueError(f"the stream is of cuda:{stream.device_index}, "
+                         f"the current device is cuda:{dev}")
     for t in own:
         if t is not None:
             t.record_stream(stream)
     return stream.cuda_stream
-
-
-def _addr(t):
-    return None if t is None else t.data_ptr()
 
 
 def ssa_page_plan(have, want, page_table, ring, pool, B: int, max_new: int, keep=None, got=None,
@@ -549,53 +548,50 @@ def ssa_page_plan(have, want, page_table, ring, pool, B: int, max_new: int, keep
     ``keep``: ``[batch]`` leading blocks that are not freed.  ``got=have`` and
     ``pool_out=pool`` update these in place.
     """
-    dev = have.device
+    i32, dev = torch.int32, _device()
     batch, max_blocks = page_table.shape
-    if got is None:
-        got = torch.empty(batch, dtype=torch.int32, device=dev)
-    if cu is None:
-        cu = torch.empty(batch + 1, dtype=torch.int32, device=dev)
-    if slots is None:
-        slots = torch.empty(max_new, dtype=torch.int32, device=dev)
-    if pool_out is None:
-        pool_out = torch.empty(2, dtype=torch.int32, device=dev)
-    args = {"have": have, "want": want, "keep": keep, "page_table": page_table, "ring": ring,
-            "pool": pool, "got": got, "cu": cu, "slots": slots, "pool_out": pool_out}
-    _on_current_device(args)
-    _i32(args)
-    for n, w in (("have", (batch,)), ("want", (batch,)), ("keep", (batch,)), ("got", (batch,)),
-                 ("cu", (batch + 1,)), ("slots", (max_new,)), ("pool", (2,)),
-                 ("pool_out", (2,)), ("ring", (ring.numel(),))):
-        _shape(args[n], n, w)
-    _check("ssa_page_plan", load_library().ssa_page_plan(
-        _addr(have), _addr(want), _addr(keep), batch, B, _addr(page_table), max_blocks,
-        ring.numel(), _addr(ring), _addr(pool), _addr(pool_out), _addr(got), _addr(cu),
-        _addr(slots), max_new, _launch_on(stream)))
+    num_pages = ring.numel()
+    rows = (batch,)
+    own = []
+    if got is None or cu is None or slots is None or pool_out is None:
+        def new(t, n):
+            if t is None:
+                t = torch.empty(n, dtype=i32, device=have.device)
+                own.append(t)
+            return t
+
+        got, cu, slots, pool_out = new(got, batch), new(cu, batch + 1), new(slots, max_new), \
+            new(pool_out, 2)
+    status = load_library().ssa_page_plan(
+        _arg("have", have, i32, rows, dev), _arg("want", want, i32, rows, dev),
+        None if keep is None else _arg("keep", keep, i32, rows, dev), batch, B,
+        _arg("page_table", page_table, i32, (batch, max_blocks), dev), max_blocks, num_pages,
+        _arg("ring", ring, i32, (num_pages,), dev), _arg("pool", pool, i32, (2,), dev),
+        _arg("pool_out", pool_out, i32, (2,), dev), _arg("got", got, i32, rows, dev),
+        _arg("cu", cu, i32, (batch + 1,), dev), _arg("slots", slots, i32, (max_new,), dev), max_new,
+        _launch_on(stream, dev, *own))
+    _check("ssa_page_plan", status)
     return got, cu, slots, pool_out
 
 
-def _q8_format(Kp: torch.Tensor, Vp: torch.Tensor) -> int:
-    if Kp.dtype != Vp.dtype:
-        raise TypeError(f"Kp and Vp must have one dtype, not {Kp.dtype} and {Vp.dtype}")
-    if Kp.dtype == torch.float8_e4m3fn:
-        return SSA_E4M3
-    if Kp.dtype == torch.int8:
-        return SSA_I8
-    raise TypeError(f"unsupported cache dtype {Kp.dtype} (float8_e4m3fn or int8)")
+_Q8_FORMATS = {torch.float8_e4m3fn: SSA_E4M3, torch.int8: SSA_I8}
 
 
-def _q8_cache(Kp, Ks, Vp, Vs, S, B: int, batch: int, max_blocks: int):
-    """Checks of the cache tensors; returns ``(num_pages, Hkv, d)``."""
+def _q8_format(Kp: torch.Tensor) -> int:
+    fmt = _Q8_FORMATS.get(Kp.dtype)
+    if fmt is None:
+        raise TypeError(f"unsupported cache dtype {Kp.dtype} (float8_e4m3fn or int8)")
+    return fmt
+
+
+def _q8_cache(Kp, Ks, Vp, Vs, B: int, dev: int):
+    """The format, sizes and addresses of the cache tensors."""
+    fmt = _q8_format(Kp)
     num_pages, Hkv, _, d = Kp.shape
-    _shape(Kp, "Kp", (num_pages, Hkv, B, d))
-    _shape(Vp, "Vp", (num_pages, Hkv, B, d))
-    _shape(Ks, "Ks", (num_pages, Hkv))
-    _shape(Vs, "Vs", (num_pages, Hkv))
-    _shape(S, "S", (batch, Hkv, max_blocks, d))
-    for n, t in (("Ks", Ks), ("Vs", Vs), ("S", S)):
-        if t is not None and t.dtype != torch.float32:
-            raise TypeError(f"{n} must be float32, not {t.dtype}")
-    return num_pages, Hkv, d
+    pool, scales = (num_pages, Hkv, B, d), (num_pages, Hkv)
+    return (fmt, num_pages, Hkv, d, _arg("Kp", Kp, Kp.dtype, pool, dev),
+            _arg("Ks", Ks, torch.float32, scales, dev), _arg("Vp", Vp, Kp.dtype, pool, dev),
+            _arg("Vs", Vs, torch.float32, scales, dev))
 
 
 def ssa_append_paged_q8(Kp, Ks, Vp, Vs, S, slots, cu, seqlens, k_new, v_new, B: int,
@@ -610,33 +606,31 @@ def ssa_append_paged_q8(Kp, Ks, Vp, Vs, S, slots, cu, seqlens, k_new, v_new, B: 
     ``k_new``/``v_new``: ``[T, Hkv, d]`` with ``T = len(slots)``, of equal strides
     and contiguous in d.
     """
-    batch = seqlens.shape[0]
+    i32, dev = torch.int32, _device()
+    batch, T = seqlens.shape[0], slots.numel()
+    fmt, num_pages, Hkv, d, kp, ks, vp, vs = _q8_cache(Kp, Ks, Vp, Vs, B, dev)
     if S is not None:
         max_blocks = S.shape[2]
     elif max_blocks is None:
         raise ValueError("max_blocks is needed when there are no summaries")
-    _on_current_device({"Kp": Kp, "Ks": Ks, "Vp": Vp, "Vs": Vs, "S": S, "slots": slots, "cu": cu,
-                        "seqlens": seqlens})
-    _i32({"slots": slots, "cu": cu, "seqlens": seqlens})
-    num_pages, Hkv, d = _q8_cache(Kp, Ks, Vp, Vs, S, B, batch, max_blocks)
-    T = slots.numel()
-    _shape(cu, "cu", (batch + 1,))
-    for n, t in (("k_new", k_new), ("v_new", v_new)):
-        if not t.is_cuda or t.get_device() != Kp.get_device():
-            raise ValueError(f"{n} must be on the device of the cache")
-        _shape(t, n, (T, Hkv, d))
-        if t.dtype != k_new.dtype:
-            raise TypeError("k_new and v_new must have one dtype")
-        if T > 0 and (t.stride(2) != 1 or t.stride() != k_new.stride()):
-            raise ValueError("k_new and v_new must have equal strides and be contiguous in d")
-    _check("ssa_append_paged_q8", load_library().ssa_append_paged_q8(
-        _addr(Kp), _addr(Ks), _addr(Vp), _addr(Vs), _q8_format(Kp, Vp), _addr(S), _addr(slots),
-        _addr(cu), _addr(seqlens), _addr(k_new), _addr(v_new), _dtype_code(k_new),
-        k_new.stride(0), k_new.stride(1), batch, T, Hkv, d, B, max_blocks, num_pages,
-        _launch_on(stream)))
+    strides, new = k_new.stride(), (T, Hkv, d)
+    if (k_new.shape != new or v_new.shape != new or k_new.dtype is not v_new.dtype
+            or k_new.get_device() != dev or v_new.get_device() != dev
+            or v_new.stride() != strides or strides[2] != 1):
+        raise ValueError(f"k_new and v_new must be {list(new)} on the current device (cuda:{dev}), "
+                         "of one dtype, of equal strides and contiguous in d")
+    status = load_library().ssa_append_paged_q8(
+        kp, ks, vp, vs, fmt,
+        None if S is None else _arg("S", S, torch.float32, (batch, Hkv, max_blocks, d), dev),
+        _arg("slots", slots, i32, (T,), dev), _arg("cu", cu, i32, (batch + 1,), dev),
+        _arg("seqlens", seqlens, i32, (batch,), dev), k_new.data_ptr(), v_new.data_ptr(),
+        _dtype_code(k_new), strides[0], strides[1], batch, T, Hkv, d, B, max_blocks, num_pages,
+        _launch_on(stream, dev))
+    _check("ssa_append_paged_q8", status)
     return Kp, Ks, Vp, Vs, S
 
 
+@functools.lru_cache(maxsize=256)
 def ssa_decode_paged_q8_workspace_size(batch: int, Hq: int, Hkv: int, d: int, B: int, topk: int,
                                        max_blocks: int) -> int:
     n = ctypes.c_size_t(0)
@@ -654,38 +648,32 @@ def ssa_decode_paged_q8(q, Kp, Ks, Vp, Vs, S, page_table, seqlens, B: int, topk:
     The cache as for ``ssa_append_paged_q8``; ``page_table``: ``[batch,
     max_blocks]`` int32.  A sequence of at most ``topk`` candidate blocks attends
     all of its cache; ``S`` may be None when ``topk >= max_blocks - 2``.
+    ``workspace``: ``ssa_decode_paged_q8_workspace_size`` bytes, uint8.
     """
-    batch, Hq, d = q.shape
+    i32, dev = torch.int32, _device()
+    fmt, num_pages, Hkv, d, kp, ks, vp, vs = _q8_cache(Kp, Ks, Vp, Vs, B, dev)
+    batch, Hq, _ = heads = q.shape
     max_blocks = page_table.shape[1]
-    num_pages, Hkv, _ = _q8_cache(Kp, Ks, Vp, Vs, S, B, batch, max_blocks)
-    if scale is None:
-        scale = 1.0 / math.sqrt(d)
+    width = (topk if topk < max_blocks else max_blocks) + 2
+    own = [None, None, None]
     if O is None:
-        O = torch.empty_like(q, memory_format=torch.contiguous_format)
-    width = min(topk, max_blocks) + 2
+        own[0] = O = torch.empty(heads, dtype=q.dtype, device=q.device)
     if idx is None and want_idx:
-        idx = torch.empty(batch, Hkv, width, dtype=torch.int32, device=q.device)
-    own = None
+        own[1] = idx = torch.empty(batch, Hkv, width, dtype=i32, device=q.device)
     if workspace is None:
-        own = workspace = torch.empty(
+        own[2] = workspace = torch.empty(
             ssa_decode_paged_q8_workspace_size(batch, Hq, Hkv, d, B, topk, max_blocks),
             dtype=torch.uint8, device=q.device)
-    _on_current_device({"q": q, "Kp": Kp, "Ks": Ks, "Vp": Vp, "Vs": Vs, "S": S, "O": O,
-                        "page_table": page_table, "seqlens": seqlens, "idx": idx,
-                        "workspace": workspace})
-    _i32({"page_table": page_table, "seqlens": seqlens, "idx": idx})
-    _shape(Kp, "Kp", (num_pages, Hkv, B, d))
-    _shape(page_table, "page_table", (batch, max_blocks))
-    _shape(seqlens, "seqlens", (batch,))
-    _shape(idx, "idx", (batch, Hkv, width))
-    _shape(O, "O", (batch, Hq, d))
-    if O.dtype != q.dtype:
-        raise TypeError(f"O must be {q.dtype}, not {O.dtype}")
-    _check("ssa_decode_paged_q8", load_library().ssa_decode_paged_q8(
-        _addr(q), _dtype_code(q), _addr(Kp), _addr(Ks), _addr(Vp), _addr(Vs), _q8_format(Kp, Vp),
-        _addr(S), _addr(page_table), max_blocks, num_pages, _addr(seqlens), batch, Hq, Hkv, d, B,
-        topk, scale, _addr(O), _addr(idx), _addr(workspace),
-        workspace.numel() * workspace.element_size(), _launch_on(stream, own)))
+    status = load_library().ssa_decode_paged_q8(
+        _arg("q", q, q.dtype, (batch, Hq, d), dev), _dtype_code(q), kp, ks, vp, vs, fmt,
+        None if S is None else _arg("S", S, torch.float32, (batch, Hkv, max_blocks, d), dev),
+        _arg("page_table", page_table, i32, (batch, max_blocks), dev), max_blocks, num_pages,
+        _arg("seqlens", seqlens, i32, (batch,), dev), batch, Hq, Hkv, d, B, topk,
+        d ** -0.5 if scale is None else scale, _arg("O", O, q.dtype, heads, dev),
+        None if idx is None else _arg("idx", idx, i32, (batch, Hkv, width), dev),
+        _arg("workspace", workspace, torch.uint8, (workspace.numel(),), dev), workspace.numel(),
+        _launch_on(stream, dev, *own))
+    _check("ssa_decode_paged_q8", status)
     return O, idx
 
 

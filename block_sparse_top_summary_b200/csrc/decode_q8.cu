@@ -18,12 +18,15 @@
 //      sequence and head that is split between blocks is finished by the last of
 //      them, from the blocks' partial records in order.
 //
-// Fragments.  m16n8k16 tiles, f16 in and fp32 out: rows 0-7 are the group's query
-// heads, rows 8-15 the same heads' low parts, so that q (fp32) and P are held as
-// the sum of two f16, 22 bits, at no further cost.  A thread reads 16 bytes of
-// a key row at a time: the tile's k index runs over the coordinates in an order of
-// our choosing, the same for q.  The key order of a tile is pi(n), chosen with the
-// chunk swizzle so that neither K nor V reads have bank conflicts.
+// Fragments.  m16n8k16 tiles, f16 in and fp32 out, with the cache as the row operand:
+// S^T = K q^T has a tile's 16 rows for the slice's keys and its 8 columns for the
+// group's heads, O^T = V^T P^T its rows for 16 coordinates.  So no row is idle, and
+// the f16 pairs of a code word are its operands as they come.  q (fp32) and P are
+// held as the sum of two f16, 22 bits: two products with one row operand and one
+// accumulator.  A thread reads 16 bytes of a key row at a time: the order of the
+// coordinates within a product is free, as long as q has the same.  The order of
+// the keys is pi(row), chosen with the chunk swizzle so that neither K nor V
+// reads have bank conflicts.  P^T is the S^T tile transposed (movmatrix).
 #include "common.cuh"
 #include "kernels.h"
 #include "q8.cuh"
@@ -36,7 +39,9 @@ namespace {
 constexpr int kQW = 12;                 // warps of the split kernel
 constexpr int kQThreads = 32 * kQW;
 constexpr int kSlice = 16;              // keys a slice
-constexpr int kQGridMax = 512;
+constexpr int kQGridMax = 256;          // most blocks of the split grid
+// Slices in flight or in use a warp: 144 KB (d = 128) or 192 KB (d = 64) a block.
+__host__ __device__ constexpr int q8_stages(int d) { return d == 128 ? 3 : 8; }
 
 // Slices of the pairs (sequence, KV head) of one sequence: s blocks, the last
 // of them with `tail` keys.
@@ -58,9 +63,32 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src, int bytes) {
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// The first `bytes` (0 or 16) from src, zeros for the rest.
+__device__ __forceinline__ void cp16_part(uint32_t dst, const void* src, int bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
                : "memory");
+}
+
+__device__ __forceinline__ uint4 lds16(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(at));
+  return v;
+}
+
+__device__ __forceinline__ uint2 lds8(uint32_t at) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at));
+  return v;
+}
+
+__device__ __forceinline__ void cp4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 
 __device__ __forceinline__ void mma16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -70,6 +98,16 @@ __device__ __forceinline__ void mma16(float (&c)[4], uint32_t a0, uint32_t a1, u
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// c = A . B (no accumulator to clear).
+__device__ __forceinline__ void mma16_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                            uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
 __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
@@ -85,7 +123,32 @@ __device__ __forceinline__ void split_half2(float a, float b, uint32_t& hi, uint
   lo = half2_bits(a - f.x, b - f.y);
 }
 
-// Key of a tile's column n.  Bits (n2 n1 n0) -> (n0 ^ n1, n2, n1).
+// Programmatic dependent launch: a kernel lets the next one of its stream start, and
+// that one waits here until the first has ended and its writes are visible.
+__device__ __forceinline__ void grid_launch_next() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Four outputs v * f on end.
+__device__ __forceinline__ void store4(float* p, float4 v, float f) {
+  *reinterpret_cast<float4*>(p) = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
+}
+__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v, float f) {
+  const __nv_bfloat162 a = __floats2bfloat162_rn(v.x * f, v.y * f);
+  const __nv_bfloat162 b = __floats2bfloat162_rn(v.z * f, v.w * f);
+  *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a),
+                                            *reinterpret_cast<const uint32_t*>(&b));
+}
+
+// The 8 x 8 tile of 16-bit values held by the warp, transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+// Key of row n (0 .. 7) of a tile.  Bits (n2 n1 n0) -> (n0 ^ n1, n2, n1).
 __device__ __forceinline__ int key_of(int n) {
   return (((n ^ (n >> 1)) & 1) << 2) | ((n >> 2) << 1) | ((n >> 1) & 1);
 }
@@ -114,6 +177,7 @@ __global__ void __launch_bounds__(256, 2) q8_route_kernel(
   __shared__ int sbuf[16];
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const int bg = blockIdx.x;
+  grid_launch_next();  // the split kernel's blocks may come in as these leave
   if (bg == batch * Hkv) {
     // slices of the sequences before each, per KV head
     int base = 0;
@@ -191,28 +255,44 @@ __global__ void __launch_bounds__(256, 2) q8_route_kernel(
 }
 
 // --------------------------------------------------------- 2. split attention
-// Partial record: m[G], l[G], o[G][D] (log2 domain, o unnormalised); a block of the
-// grid owns two, for the pair that begins before its run and for the one that goes
-// on behind it.
+// The state of a warp, a block or the whole pair: m[G'], l[G'], o[G'][D] (log2 domain,
+// o unnormalised).  Records of warps are in shared memory (G' = 8), those of blocks
+// in the workspace (G' = G); a block of the grid owns two, for the pair that
+// begins before its run and for the one that goes on behind it.
 template <typename T, int D, int F>
 __global__ void __launch_bounds__(kQThreads, 1) q8_split_kernel(
     const T* __restrict__ q, const uint8_t* __restrict__ Kp, const float* __restrict__ Ks,
     const uint8_t* __restrict__ Vp, const float* __restrict__ Vs,
     const int32_t* __restrict__ table, const int32_t* __restrict__ seqlens, int batch, int Hq,
-    int Hkv, int B, int max_blocks, int num_pages, int kk, int width, int stages, int min_slices,
+    int Hkv, int B, int max_blocks, int num_pages, int kk, int width, int min_slices,
     const int32_t* __restrict__ ws_idx, const int32_t* __restrict__ ws_off,
     float* __restrict__ ws_part, int* __restrict__ ws_ctr, T* __restrict__ O, float scale_log2) {
   constexpr int TILE = kSlice * D;       // bytes of K (or V) of a slice
   constexpr int KS = D / 16;             // k steps of S
-  constexpr int ON = D / 8;              // column tiles of O
+  constexpr int OT = D / 16;             // tiles of O^T
   constexpr int CPR = D / 16;            // 16-byte chunks of a row
   constexpr int NCP = kSlice * CPR / 32; // chunks a lane copies
-  constexpr float kLazy = 8.0f;          // O is rescaled when the maximum grows by more
+  constexpr int REC = 8 * (D + 2);       // floats of a warp's record
+  // P stays below 2^(kLazy + kUp + 3) = 2^15, within f16: O is rescaled when the
+  // maximum grows by more than kLazy (log2), or V's scale leaves [vref / 8, 8 vref]
+  constexpr float kLazy = 8.0f, kUp = 4.0f, kNear = 8.0f;
+  constexpr int stages = q8_stages(D);
+  static_assert(stages * 2 * TILE >= REC * 4, "a warp's ring holds its record");
+  // floats of the sums that the last block's threads exchange: [PS - 1][E][8]
+  constexpr int kJoinSums = (kQW * REC - 2 * 8 * kQGridMax) / 8;
+  static_assert(kJoinSums >= 8 * (D / 4), "one float4 of each head for one thread at least");
+  // q in fp32 keeps a low part; bf16 is exact in f16
+  constexpr bool kLow = sizeof(T) == 4;
   extern __shared__ __align__(128) unsigned char q8_smem[];
-  __shared__ int s_last, s_b;
+  __shared__ int s_b, s_groups;
+  __shared__ int s_pair[kQW][2];             // pair of a warp's first and last record, or -1
+  __shared__ int s_list[2 * kQW];            // records in use
+  __shared__ int s_from[kQW + 2], s_gpair[kQW + 1];  // a group's records in s_list, its pair
+  __shared__ int s_last[2];
 
-  const int G = Hq / Hkv, Lmax = max_blocks * B, spb = B / kSlice;
+  const int G = Hq / Hkv, spb = B / kSlice;
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  grid_wait();  // the route kernel's results
   const long long total = (long long)ws_off[batch] * Hkv;
   // no more blocks than leave each some slices
   const long long most = (total + min_slices - 1) / min_slices;
@@ -220,37 +300,30 @@ __global__ void __launch_bounds__(kQThreads, 1) q8_split_kernel(
   if (blockIdx.x >= grid) return;  // also when there is nothing at all
   const long long s0 = blockIdx.x * total / grid, s1 = (blockIdx.x + 1) * total / grid;
   const int ns = (int)(s1 - s0);
+  // the warp's run
+  const int w0 = (int)((long long)warp * ns / kQW), w1 = (int)((long long)(warp + 1) * ns / kQW);
 
-  uint4* qf = reinterpret_cast<uint4*>(q8_smem);                         // [KS][32]
-  float* qx = reinterpret_cast<float*>(q8_smem + KS * 32 * 16);          // [8]
-  float* mw = qx + 8;                                                    // [kQW][8]
-  float* lw = mw + kQW * 8;                                              // [kQW][8]
-  float* ow = lw + kQW * 8;                                              // [kQW][8][D]
-  float4* meta = reinterpret_cast<float4*>(ow + kQW * 8 * D);            // [kQW][stages]
-  unsigned char* ring0 = reinterpret_cast<unsigned char*>(meta + kQW * 8);
-  unsigned char* ring = ring0 + (size_t)warp * stages * 2 * TILE;
-  float4* minfo = meta + warp * 8;
+  unsigned char* ring = q8_smem + (size_t)warp * stages * 2 * TILE;  // [kQW][stages][K, V]
+  float* rec0 = reinterpret_cast<float*>(q8_smem + (size_t)kQW * stages * 2 * TILE);  // [kQW][REC]
+  float4* minfo = reinterpret_cast<float4*>(rec0 + kQW * REC) + warp * 8;  // [kQW][8]: rows, ks, vs
 
-  // the sequence of slice s: the last b with off[b] Hkv <= s
-  if (t == 0) s_b = 0;
-  __syncthreads();
+  // the sequence of the block's first slice
+  if (t < kQW * 2) s_pair[t >> 1][t & 1] = -1;
   for (int b0 = 0; b0 < batch; b0 += kQThreads) {
     const int b = b0 + t;
-    const bool in = b < batch && (long long)ws_off[b] * Hkv <= s0 &&
-                    (long long)ws_off[b + 1] * Hkv > s0;
-    if (in) s_b = b;
+    if (b < batch && (long long)ws_off[b] * Hkv <= s0 && (long long)ws_off[b + 1] * Hkv > s0)
+      s_b = b;
   }
   __syncthreads();
   const int b_first = s_b;
 
-  // What a slice is: pair, page * Hkv + g (or -1), first row, rows.
+  // What a slice is: page * Hkv + g (or -1: no keys), first row | rows << 8.
   struct Slice {
-    int pg, row, rows;
-    float ks, vs;
+    int pg, rows;
   };
   auto resolve = [&](int i) -> Slice {
-    Slice r{-1, 0, 0, 0.f, 0.f};
-    if (i >= ns) return r;
+    Slice r{-1, 0};
+    if (i >= w1) return r;
     const long long s = s0 + i;
     int b = b_first;
     while ((long long)ws_off[b + 1] * Hkv <= s) ++b;
@@ -263,288 +336,449 @@ __global__ void __launch_bounds__(kQThreads, 1) q8_split_kernel(
     const int j = last - 1 > kk ? ws_idx[((int64_t)b * Hkv + g) * width + e] : e;
     const int rows = min(kSlice, L - j * B - sub * kSlice);
     const int page = table[(int64_t)b * max_blocks + j];
-    if (page < 0 || page >= num_pages || rows <= 0) return r;  // no page: no keys
+    if (page < 0 || page >= num_pages || rows <= 0) return r;
     r.pg = page * Hkv + g;
-    r.row = sub * kSlice;
-    r.rows = rows;
-    r.ks = Ks[r.pg];
-    r.vs = Vs[r.pg];
+    r.rows = sub * kSlice | rows << 8;
     return r;
   };
 
-  // Warp w takes slices w, w + kQW, ...; lane l resolves the warp's slice 32 c + l.
-  Slice cur = resolve(warp + lane * kQW), nxt = resolve(warp + (32 + lane) * kQW);
-  auto issue = [&](int n) {  // the warp's n-th slice into stage n % stages
-    if (warp + n * kQW < ns) {
-      const int src = n & 31;
-      const int pg = __shfl_sync(0xffffffffu, cur.pg, src);
-      const int row = __shfl_sync(0xffffffffu, cur.row, src);
-      const int rows = __shfl_sync(0xffffffffu, cur.rows, src);
-      const float ks = __shfl_sync(0xffffffffu, cur.ks, src);
-      const float vs = __shfl_sync(0xffffffffu, cur.vs, src);
-      const int st = n % stages;
-      if (rows > 0) {
-        const uint32_t dk = (uint32_t)__cvta_generic_to_shared(ring + (size_t)st * 2 * TILE);
-        const int64_t base = ((int64_t)pg * B + row) * D;
+  // Lane l resolves the warp's slice 32 c + l, a batch ahead of its use.
+  Slice cur = resolve(w0 + lane), nxt = resolve(w0 + 32 + lane);
+  // A slice is 16 rows of d bytes on end: lane l copies the chunks l, l + 32, ...,
+  // row l / CPR + 32 i / CPR, whose swizzle depends on i only by its parity.
+  const uint32_t ring_s = (uint32_t)__cvta_generic_to_shared(ring);
+  const uint32_t info_s = (uint32_t)__cvta_generic_to_shared(minfo);
+  uint32_t kdst[2], vdst[2];
 #pragma unroll
-        for (int i = 0; i < NCP; ++i) {
-          const int c = lane + 32 * i, r = c / CPR, cc = c % CPR;
+  for (int i = 0; i < 2; ++i) {
+    const int c = lane + 32 * (i % NCP);
+    kdst[i] = ring_s + tile_at<D, false>(c / CPR, c % CPR);
+    vdst[i] = ring_s + TILE + tile_at<D, true>(c / CPR, c % CPR);
+  }
+  auto issue = [&](int n, int st) {  // the warp's n-th slice into stage st = n % stages
+    if (w0 + n < w1) {
+      const int pg = __shfl_sync(0xffffffffu, cur.pg, n & 31);
+      const int rr = __shfl_sync(0xffffffffu, cur.rows, n & 31);
+      const int rows = rr >> 8;
+      if (pg >= 0) {
+        const int64_t at = ((int64_t)pg * B + (rr & 255)) * D + lane * 16;
+        const uint32_t so = (uint32_t)st * (2 * TILE);
+        if (rows == kSlice) {
+#pragma unroll
+          for (int i = 0; i < NCP; ++i) {
+            cp16(kdst[i & 1] + so + (i >> 1) * 1024, Kp + at + i * 512);
+            cp16(vdst[i & 1] + so + (i >> 1) * 1024, Vp + at + i * 512);
+          }
+        } else {
           // rows past the sequence read as zeros
-          const int64_t src_at = base + (r < rows ? r : 0) * D + cc * 16;
-          const int bytes = r < rows ? 16 : 0;
-          cp16(dk + tile_at<D, false>(r, cc), Kp + src_at, bytes);
-          cp16(dk + TILE + tile_at<D, true>(r, cc), Vp + src_at, bytes);
+#pragma unroll
+          for (int i = 0; i < NCP; ++i) {
+            const bool in = (lane + 32 * i) / CPR < rows;
+            const int64_t from = in ? at + i * 512 : at - lane * 16;
+            cp16_part(kdst[i & 1] + so + (i >> 1) * 1024, Kp + from, in ? 16 : 0);
+            cp16_part(vdst[i & 1] + so + (i >> 1) * 1024, Vp + from, in ? 16 : 0);
+          }
         }
+        if (lane < 2) cp4(info_s + st * 16 + 4 + 4 * lane, (lane ? Vs : Ks) + pg);
       }
-      if (lane == 0) minfo[st] = make_float4(__int_as_float(rows), ks, vs, 0.f);
+      if (lane == 2) minfo[st].x = __int_as_float(rows);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
     if ((n & 31) == 31) {
       cur = nxt;
-      nxt = resolve(warp + (n + 33 + lane) * kQW);
+      nxt = resolve(w0 + n + 33 + lane);
     }
   };
-  for (int n = 0; n < stages - 1; ++n) issue(n);
+  for (int n = 0; n < stages - 1; ++n) issue(n, n);
 
   const int gr = lane >> 2, tq = lane & 3;
-  const int key0 = key_of(gr);                 // K row of this lane (tile 0)
-  const int va = key_of(2 * tq), vb = key_of(2 * tq + 1);
-  float oc[ON][2];
-  int n = 0;  // the warp's next slice
-
+  const int ka = key_of(gr), va = key_of(2 * tq), vb = key_of(2 * tq + 1);
+  // this lane's chunks of a slice: K row ka (and 8 on; the
+  // second half of a row of 128 at ^ 64), V rows va, vb (and 8 on), columns of gr
+  const uint32_t k_at = ring_s + tile_at<D, false>(ka, tq);
+  const uint32_t k_at2 = D == 128 ? k_at ^ 64u : k_at;
+  const uint32_t v_at = ring_s + TILE + (D == 128 ? tile_at<D, true>(va, gr)
+                                                  : tile_at<D, true>(va, gr >> 1) + 8 * (gr & 1));
+  const uint32_t v_at2 = ring_s + TILE + (D == 128 ? tile_at<D, true>(vb, gr)
+                                                   : tile_at<D, true>(vb, gr >> 1) + 8 * (gr & 1));
+  // O^T: [i][e + 2 y] is head 2 tq + e, coordinate gr D / 8 + 2 i + y
+  float oc[OT][4];
+  int n = 0, st = 0;  // the warp's next slice and its stage
   int b = b_first;
-  long long pos = s0;
-  while (pos < s1) {
-    // ---- the pair at slice pos
+  while (w0 + n < w1) {
+    // ---- the pair at the warp's slice n
+    const long long pos = s0 + w0 + n;
     while ((long long)ws_off[b + 1] * Hkv <= pos) ++b;
     const int per = ws_off[b + 1] - ws_off[b];
     const int g = (int)((pos - (long long)ws_off[b] * Hkv) / per);
     const long long pair0 = (long long)ws_off[b] * Hkv + (long long)g * per;
-    const long long pair1 = pair0 + per;
-    const long long end = pair1 < s1 ? pair1 : s1;
-    // its queries: a power of two brings each head's largest coordinate into
-    // [2^14, 2^15), and two f16 hold the rest
-    __syncthreads();  // the last pair's q and merge buffers are free
-    if (warp < 8) {
-      float v[D / 32], m = 0.f;
+    const bool begins = pair0 >= s0 + w0, ends = pair0 + per <= s0 + w1;
+    const int stop = ends ? (int)(pair0 + per - s0) - w0 : w1 - w0;
+
+    // Fragments of q.  Lane (gr, tq) holds coordinates 64 c + 16 tq + 4 s + i of
+    // head gr: k step 4 c + s, words b0 (i < 2) and b1; a power of two brings
+    // the head's largest coordinate into [2^14, 2^15).
+    uint32_t qa[KS][2], ql[kLow ? KS : 1][2];
+    float qscale[2];  // of heads 2 tq and 2 tq + 1
+    {
+      float v[D / 64][16], m = 0.f;
+      const T* qp = q + ((int64_t)b * Hq + g * G + (gr < G ? gr : 0)) * D + 16 * tq;
 #pragma unroll
-      for (int e = 0; e < D / 32; ++e) {
-        v[e] = warp < G ? (float)q[((int64_t)b * Hq + g * G + warp) * D + lane + 32 * e] : 0.f;
-        m = fmaxf(m, fabsf(v[e]));
+      for (int c = 0; c < D / 64; ++c) {
+#pragma unroll
+        for (int e = 0; e < 16; e += Vec16<T>::n) unpack16(ldg16(qp + 64 * c + e), v[c] + e, qp);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          v[c][e] = gr < G ? v[c][e] : 0.f;
+          m = fmaxf(m, fabsf(v[c][e]));
+        }
       }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      int ex = (int)(__float_as_uint(m) >> 23) - 127 - 14;
-      ex = max(ex, -126);
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+      const int ex = max((int)(__float_as_uint(m) >> 23) - 127 - 14, -126);
       const float up = __uint_as_float((uint32_t)(127 - ex) << 23);
-      if (lane == 0) qx[warp] = __uint_as_float((uint32_t)(127 + ex) << 23) * scale_log2;
-      // coordinate dd = 64 c + 16 tq' + 4 s + i of head h: k step 4 c + s, lane
-      // 4 h + tq', half i of the pair of words (a0, a2)
+      const float back = __uint_as_float((uint32_t)(127 + ex) << 23) * scale_log2;
+      qscale[0] = __shfl_sync(0xffffffffu, back, 8 * tq);
+      qscale[1] = __shfl_sync(0xffffffffu, back, 8 * tq + 4);
 #pragma unroll
-      for (int e = 0; e < D / 32; ++e) {
-        const int dd = lane + 32 * e;
-        const int ks = (dd >> 6) * 4 + ((dd >> 2) & 3), ln = warp * 4 + ((dd >> 4) & 3);
-        const float y = v[e] * up;
-        const __half hi = __float2half_rn(y);
-        const __half lo = __float2half_rn(y - __half2float(hi));
-        __half* w = reinterpret_cast<__half*>(qf + ks * 32 + ln);
-        const int i = dd & 3;
-        w[(i >> 1) * 4 + (i & 1)] = hi;       // a0 or a2
-        w[(i >> 1) * 4 + 2 + (i & 1)] = lo;   // a1 or a3
+      for (int ks = 0; ks < KS; ++ks) {
+        const float* x = v[ks >> 2] + 4 * (ks & 3);
+        if constexpr (kLow) {
+          split_half2(x[0] * up, x[1] * up, qa[ks][0], ql[ks][0]);
+          split_half2(x[2] * up, x[3] * up, qa[ks][1], ql[ks][1]);
+        } else {
+          qa[ks][0] = half2_bits(x[0] * up, x[1] * up);
+          qa[ks][1] = half2_bits(x[2] * up, x[3] * up);
+        }
       }
     }
-    __syncthreads();
-    const float qscale = qx[gr];
-    float m_run = -INFINITY, l_run = 0.f;
+    float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
+    // O is kept in units of vref, a scale of V met so far
+    float vref = 1.f, vinv = 1.f;
 #pragma unroll
-    for (int i = 0; i < ON; ++i) oc[i][0] = oc[i][1] = 0.f;
+    for (int i = 0; i < OT; ++i) oc[i][0] = oc[i][1] = oc[i][2] = oc[i][3] = 0.f;
 
-    for (; s0 + warp + (long long)n * kQW < end; ++n) {
-      issue(n + stages - 1);
-      if (stages == 8) asm volatile("cp.async.wait_group 7;" ::: "memory");
-      else if (stages == 4) asm volatile("cp.async.wait_group 3;" ::: "memory");
-      else asm volatile("cp.async.wait_group 2;" ::: "memory");
+    for (; n < stop; ++n) {
+      issue(n + stages - 1, st == 0 ? stages - 1 : st - 1);
+      asm volatile("cp.async.wait_group %0;" ::"n"(stages - 1) : "memory");
       __syncwarp();
-      const int st = n % stages;
       const float4 mi = minfo[st];
       const int rows = __float_as_int(mi.x);
-      const unsigned char* kt = ring + (size_t)st * 2 * TILE;
-      const unsigned char* vt = kt + TILE;
+      const uint32_t so = (uint32_t)st * (2 * TILE);
       if (rows > 0) {
-        // S = q . K^T of 16 keys
-        float sc[2][4];
-#pragma unroll
-        for (int x = 0; x < 2; ++x) sc[x][0] = sc[x][1] = sc[x][2] = sc[x][3] = 0.f;
+        // S^T = K q^T of 16 keys, even and odd k steps apart
+        float se[4], sd[4];
 #pragma unroll
         for (int c = 0; c < D / 64; ++c) {
-          uint4 w[2];
-#pragma unroll
-          for (int x = 0; x < 2; ++x)
-            w[x] = *reinterpret_cast<const uint4*>(kt + tile_at<D, false>(key0 + 8 * x, 4 * c + tq));
+          const uint4 u = lds16((c == 0 ? k_at : k_at2) + so);
+          const uint4 v = lds16((c == 0 ? k_at : k_at2) + so + 8 * D);
 #pragma unroll
           for (int s = 0; s < 4; ++s) {
-            const uint4 a = qf[(4 * c + s) * 32 + lane];
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              uint32_t b0, b1;
-              q8_to_half4<F>(s == 0 ? w[x].x : s == 1 ? w[x].y : s == 2 ? w[x].z : w[x].w, b0, b1);
-              mma16(sc[x], a.x, a.y, a.z, a.w, b0, b1);
-            }
+            uint32_t a0, a1, a2, a3;
+            q8_to_half4<F>(s == 0 ? u.x : s == 1 ? u.y : s == 2 ? u.z : u.w, a0, a2);
+            q8_to_half4<F>(s == 0 ? v.x : s == 1 ? v.y : s == 2 ? v.z : v.w, a1, a3);
+            const int ks = 4 * c + s;
+            if (ks == 0) mma16_first(se, a0, a1, a2, a3, qa[ks][0], qa[ks][1]);
+            else if (ks == 1) mma16_first(sd, a0, a1, a2, a3, qa[ks][0], qa[ks][1]);
+            else mma16(s & 1 ? sd : se, a0, a1, a2, a3, qa[ks][0], qa[ks][1]);
+            if constexpr (kLow) mma16(s & 1 ? sd : se, a0, a1, a2, a3, ql[ks][0], ql[ks][1]);
           }
         }
-        // softmax over the row's keys, log2 domain
-        const float f = mi.y * qscale;
-        float cm = -INFINITY;
+        uint32_t r[4][D / 32];  // V rows va, vb, va + 8, vb + 8: columns gr D / 8 ...
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int key = 8 * x + (e == 0 ? va : vb);
-            const float y = key < rows ? (sc[x][e] + sc[x][e + 2]) * f : -INFINITY;
-            sc[x][e] = y;
-            cm = fmaxf(cm, y);
-          }
-        cm = fmaxf(cm, __shfl_xor_sync(0xffffffffu, cm, 1));
-        cm = fmaxf(cm, __shfl_xor_sync(0xffffffffu, cm, 2));
-        if (cm > m_run + kLazy) {
-          const float alpha = ex2(m_run - cm);  // 0 on the first slice
-          l_run *= alpha;
-#pragma unroll
-          for (int i = 0; i < ON; ++i) {
-            oc[i][0] *= alpha;
-            oc[i][1] *= alpha;
-          }
-          m_run = cm;
-        }
-        __syncwarp();
-        const float mr = m_run == -INFINITY ? 0.f : m_run;
-        float p[2][2];
-#pragma unroll
-        for (int x = 0; x < 2; ++x)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            p[x][e] = ex2(sc[x][e] - mr);
-            l_run += p[x][e];
-          }
-        uint32_t a0, a1, a2, a3;
-        split_half2(p[0][0], p[0][1], a0, a1);
-        split_half2(p[1][0], p[1][1], a2, a3);
-        // O += vs (P . V): lane's columns are d = gr * (D / 8) + i
-        const float vs = mi.z;
-#pragma unroll
-        for (int hw = 0; hw < D / 64; ++hw) {
-          // d = 128: one 16-byte chunk a row, in two halves; d = 64: 8 bytes a row
-          uint2 r0, r1, r2, r3;
+        for (int y = 0; y < 4; ++y) {
+          const uint32_t at = (y & 1 ? v_at2 : v_at) + so + (y >> 1) * (8 * D);
           if constexpr (D == 128) {
-            r0 = *reinterpret_cast<const uint2*>(vt + tile_at<D, true>(va, gr) + 8 * hw);
-            r1 = *reinterpret_cast<const uint2*>(vt + tile_at<D, true>(vb, gr) + 8 * hw);
-            r2 = *reinterpret_cast<const uint2*>(vt + tile_at<D, true>(va + 8, gr) + 8 * hw);
-            r3 = *reinterpret_cast<const uint2*>(vt + tile_at<D, true>(vb + 8, gr) + 8 * hw);
+            const uint4 w = lds16(at);
+            r[y][0] = w.x; r[y][1] = w.y; r[y][2 % (D / 32)] = w.z; r[y][3 % (D / 32)] = w.w;
           } else {
-            r0 = *reinterpret_cast<const uint2*>(vt + tile_at<D, true>(va, gr >> 1) + 8 * (gr & 1));
-            r1 = *reinterpret_cast<const uint2*>(vt + tile_at<D, true>(vb, gr >> 1) + 8 * (gr & 1));
-            r2 = *reinterpret_cast<const uint2*>(vt + tile_at<D, true>(va + 8, gr >> 1) + 8 * (gr & 1));
-            r3 = *reinterpret_cast<const uint2*>(vt + tile_at<D, true>(vb + 8, gr >> 1) + 8 * (gr & 1));
-          }
-#pragma unroll
-          for (int w = 0; w < 2; ++w) {
-            const uint32_t x0 = w ? r0.y : r0.x, x1 = w ? r1.y : r1.x;
-            const uint32_t x2 = w ? r2.y : r2.x, x3 = w ? r3.y : r3.x;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              // bytes (2 h, 2 h + 1) of the two rows, paired by column
-              const uint32_t sel = h ? 0x7362 : 0x5140;
-              uint32_t e0, e1, f0, f1;
-              q8_to_half4<F>(__byte_perm(x0, x1, sel), e0, e1);
-              q8_to_half4<F>(__byte_perm(x2, x3, sel), f0, f1);
-              const int i = hw * 8 + w * 4 + h * 2;
-              float c0[4] = {0.f, 0.f, 0.f, 0.f}, c1[4] = {0.f, 0.f, 0.f, 0.f};
-              mma16(c0, a0, a1, a2, a3, e0, f0);
-              mma16(c1, a0, a1, a2, a3, e1, f1);
-              oc[i][0] = fmaf(c0[0] + c0[2], vs, oc[i][0]);
-              oc[i][1] = fmaf(c0[1] + c0[3], vs, oc[i][1]);
-              oc[i + 1][0] = fmaf(c1[0] + c1[2], vs, oc[i + 1][0]);
-              oc[i + 1][1] = fmaf(c1[1] + c1[3], vs, oc[i + 1][1]);
-            }
+            const uint2 w = lds8(at);
+            r[y][0] = w.x; r[y][1] = w.y;
           }
         }
+        // softmax, log2 domain: x[y][e] is key row gr + 8 y, head 2 tq + e
+        float x[2][2];
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) x[y][e] = (se[2 * y + e] + sd[2 * y + e]) * (mi.y * qscale[e]);
+        if (rows < kSlice) {
+#pragma unroll
+          for (int y = 0; y < 2; ++y)
+            if (ka + 8 * y >= rows) x[y][0] = x[y][1] = -INFINITY;
+        }
+        const float c0 = fmaxf(x[0][0], x[1][0]), c1 = fmaxf(x[0][1], x[1][1]);
+        if (__any_sync(0xffffffffu, c0 > m_run[0] + kLazy || c1 > m_run[1] + kLazy)) {
+          float cm[2] = {c0, c1};
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1)
+              cm[e] = fmaxf(cm[e], __shfl_xor_sync(0xffffffffu, cm[e], o));
+            cm[e] = fmaxf(cm[e], m_run[e]);
+            const float alpha = m_run[e] == cm[e] ? 1.f : ex2(m_run[e] - cm[e]);  // 0 at first
+            l_run[e] *= alpha;
+#pragma unroll
+            for (int i = 0; i < OT; ++i) {
+              oc[i][e] *= alpha;
+              oc[i][e + 2] *= alpha;
+            }
+            m_run[e] = cm[e];
+          }
+        }
+        // P times the scale of V, as a factor of vref near 1
+        const float vs = mi.z;
+        float ratio = vs * vinv;
+        if (!(ratio <= kNear && ratio >= 1.f / kNear) && vs != 0.f) {
+          const float inv = 1.f / fmaxf(vs, 1.17549435e-38f);
+          const float by = vref * inv;  // O in units of vs
+          bool any = false;
+#pragma unroll
+          for (int i = 0; i < OT; ++i)
+            any |= oc[i][0] != 0.f || oc[i][1] != 0.f || oc[i][2] != 0.f || oc[i][3] != 0.f;
+          any = __any_sync(0xffffffffu, any);
+          // an O over 2^60 times what this block can add stays as it is
+          if (!(any && by > 1.152921504606847e18f)) {
+            const float f = any ? by : 0.f;
+#pragma unroll
+            for (int i = 0; i < OT; ++i) {
+              oc[i][0] *= f;
+              oc[i][1] *= f;
+              oc[i][2] *= f;
+              oc[i][3] *= f;
+            }
+            vref = vs;
+            vinv = inv;
+            ratio = vs * inv;
+          }
+        }
+        // p is raised by 2^kUp, which l has too: more of P is in f16's normal range
+        uint32_t hi[2], lo[2];
+        {
+          const float m0 = (m_run[0] == -INFINITY ? 0.f : m_run[0]) - kUp;
+          const float m1 = (m_run[1] == -INFINITY ? 0.f : m_run[1]) - kUp;
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const float p0 = ex2(x[y][0] - m0), p1 = ex2(x[y][1] - m1);
+            l_run[0] += p0;
+            l_run[1] += p1;
+            split_half2(p0 * ratio, p1 * ratio, hi[y], lo[y]);
+            hi[y] = transpose8(hi[y]);
+            lo[y] = transpose8(lo[y]);
+          }
+        }
+        // O^T += V^T P^T
+#pragma unroll
+        for (int w = 0; w < D / 32; ++w)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            // bytes (2 h, 2 h + 1) of the rows, paired by column
+            const uint32_t sel = h ? 0x7362 : 0x5140;
+            uint32_t a0, a1, a2, a3;
+            q8_to_half4<F>(__byte_perm(r[0][w], r[1][w], sel), a0, a1);
+            q8_to_half4<F>(__byte_perm(r[2][w], r[3][w], sel), a2, a3);
+            mma16(oc[2 * w + h], a0, a1, a2, a3, hi[0], hi[1]);
+            mma16(oc[2 * w + h], a0, a1, a2, a3, lo[0], lo[1]);
+          }
       }
+      st = st == stages - 1 ? 0 : st + 1;
       __syncwarp();  // the stage is read before it is filled again
     }
 
-    // ---- end of the pair in this block: join the warps
-    float l = l_run;
-    l += __shfl_xor_sync(0xffffffffu, l, 1);
-    l += __shfl_xor_sync(0xffffffffu, l, 2);
-    if (tq == 0) {
-      mw[warp * 8 + gr] = m_run;
-      lw[warp * 8 + gr] = l;
-    }
+    // ---- the pair's end in this warp
 #pragma unroll
     for (int e = 0; e < 2; ++e)
 #pragma unroll
-      for (int i = 0; i < ON; i += 4)
-        *reinterpret_cast<float4*>(ow + ((size_t)warp * 8 + gr) * D + (2 * tq + e) * ON + i) =
-            make_float4(oc[i][e], oc[i + 1][e], oc[i + 2][e], oc[i + 3][e]);
-    __syncthreads();
-    const int64_t pr = (int64_t)b * Hkv + g;
-    // blocks of the grid that hold slices of the pair
-    auto block_of = [&](long long s) { return (int)(((s + 1) * grid + total - 1) / total - 1); };
-    const int xf = block_of(pair0), xl = block_of(pair1 - 1);
-    const bool whole = xf == xl;
-    const size_t rec = (size_t)G * (D + 2);
-    float* part = ws_part + ((size_t)blockIdx.x * 2 + (pair0 < s0 ? 0 : 1)) * rec;
-    for (int e = t; e < G * D; e += kQThreads) {
-      const int h = e / D, dd = e - h * D;
-      float M = -INFINITY;
+      for (int o = 4; o < 32; o <<= 1) l_run[e] += __shfl_xor_sync(0xffffffffu, l_run[e], o);
 #pragma unroll
-      for (int w = 0; w < kQW; ++w) M = fmaxf(M, mw[w * 8 + h]);
-      float num = 0.f, den = 0.f;
+    for (int i = 0; i < OT; ++i)
 #pragma unroll
-      for (int w = 0; w < kQW; ++w) {
-        // a warp without keys weighs 0; one whose logits were NaN keeps its NaN
-        const float a = mw[w * 8 + h] == -INFINITY ? 0.f : ex2(mw[w * 8 + h] - M);
-        num = fmaf(a, ow[((size_t)w * 8 + h) * D + dd], num);
-        den = fmaf(a, lw[w * 8 + h], den);
-      }
-      if (whole) {
-        store_out(O + ((int64_t)b * Hq + g * G + h) * D + dd, den == 0.f ? 0.f : num / den);
-      } else {
-        part[2 * G + h * D + dd] = num;
-        if (dd == 0) {
-          part[h] = M;
-          part[G + h] = den;
+      for (int e = 0; e < 4; ++e) oc[i][e] *= vref;
+    const int pair = b * Hkv + g;
+    if (begins && ends) {
+      // nobody else has a part of it; no key at all gives zeros
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        if (2 * tq + e < G) {
+          const float inv = l_run[e] == 0.f ? 0.f : 1.f / l_run[e];
+          T* op = O + ((int64_t)b * Hq + g * G + 2 * tq + e) * D + gr * (D / 8);
+#pragma unroll
+          for (int i = 0; i < OT; i += 2)
+            store4(op + 2 * i, make_float4(oc[i][e], oc[i][e + 2], oc[i + 1][e], oc[i + 1][e + 2]),
+                   inv);
         }
+    } else {
+      // a pair that began before the run, or one that goes on behind it (then the
+      // warp's ring is free)
+      const int last = begins ? 1 : 0;
+      float* rec = last ? reinterpret_cast<float*>(ring) : rec0 + warp * REC;
+      if (lane == 0) s_pair[warp][last] = pair;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int h = 2 * tq + e;
+        if (gr == 0) {
+          rec[h] = m_run[e];
+          rec[8 + h] = l_run[e];
+        }
+#pragma unroll
+        for (int i = 0; i < OT; i += 2)
+          *reinterpret_cast<float4*>(rec + 16 + h * D + gr * (D / 8) + 2 * i) =
+              make_float4(oc[i][e], oc[i][e + 2], oc[i + 1][e], oc[i + 1][e + 2]);
       }
     }
-    if (!whole) {
-      __threadfence();
-      __syncthreads();
-      if (t == 0) s_last = atomicAdd(&ws_ctr[pr], 1) == xl - xf;
-      __syncthreads();
-      if (s_last) {
-        __threadfence();
-        for (int e = t; e < G * D; e += kQThreads) {
-          const int h = e / D, dd = e - h * D;
-          // the pair is the last of its first block and the first of the others
-          auto record = [&](int x) { return ws_part + ((size_t)x * 2 + (x == xf ? 1 : 0)) * rec; };
-          float M = -INFINITY;
-          for (int x = xf; x <= xl; ++x) M = fmaxf(M, __ldcg(record(x) + h));
-          float num = 0.f, den = 0.f;
-          for (int x = xf; x <= xl; ++x) {
-            const float* pp = record(x);
-            const float mx = __ldcg(pp + h);
-            const float a = mx == -INFINITY ? 0.f : ex2(mx - M);
-            num = fmaf(a, __ldcg(pp + 2 * G + h * D + dd), num);
-            den = fmaf(a, __ldcg(pp + G + h), den);
-          }
-          store_out(O + ((int64_t)b * Hq + g * G + h) * D + dd, den == 0.f ? 0.f : num / den);
-        }
-      }
-    }
-    pos = end;
   }
-  asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncthreads();
+
+  // ---- join the warps' records, pair by pair.  Record 2 w is warp w's first, 2 w + 1
+  // its last; those of a pair follow one another.
+  if (warp == 0) {
+    const int p = lane < 2 * kQW ? s_pair[lane >> 1][lane & 1] : -1;
+    const uint32_t have = __ballot_sync(0xffffffffu, p >= 0);
+    const uint32_t before = have & lanemask_lt();
+    const int prev = __shfl_sync(0xffffffffu, p, before ? 31 - __clz(before) : 0);
+    const bool first = p >= 0 && (before == 0 || prev != p);
+    const uint32_t firsts = __ballot_sync(0xffffffffu, first);
+    const int k = __popc(firsts & lanemask_lt());  // groups before this lane
+    if (p >= 0) s_list[__popc(before)] = lane;
+    if (first) {
+      s_from[k] = __popc(before);
+      s_gpair[k] = p;
+    }
+    if (lane == 0) {
+      s_groups = __popc(firsts);
+      s_from[__popc(firsts)] = __popc(have);
+    }
+  }
+  __syncthreads();
+  const int groups = s_groups;
+  const size_t rec_g = (size_t)G * D + 16;  // o[G][D], m[8], l[8]
+  // first slice of a pair, and its number of slices
+  auto pair_first = [&](int p) {
+    const int pb = p / Hkv;
+    return (long long)ws_off[pb] * Hkv + (long long)(p - pb * Hkv) * (ws_off[pb + 1] - ws_off[pb]);
+  };
+  auto pair_len = [&](int p) { return ws_off[p / Hkv + 1] - ws_off[p / Hkv]; };
+  const int E = G * (D / 4);  // float4 of a record
+  for (int e = t; e < groups * E; e += kQThreads) {
+    const int k = e / E, r = e - k * E;
+    const int h = r / (D / 4), d4 = (r - h * (D / 4)) * 4;
+    const int from = s_from[k], to = s_from[k + 1], p = s_gpair[k];
+    auto at = [&](int x) {
+      const int rc = s_list[x];
+      return rc & 1 ? reinterpret_cast<const float*>(q8_smem + (size_t)(rc >> 1) * stages * 2 * TILE)
+                    : rec0 + (rc >> 1) * REC;
+    };
+    float M = -INFINITY;
+#pragma unroll 4
+    for (int x = from; x < to; ++x) M = fmaxf(M, at(x)[h]);
+    float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
+    float den = 0.f;
+#pragma unroll 4
+    for (int x = from; x < to; ++x) {
+      const float* rc = at(x);
+      // a record without keys weighs 0; one whose logits were NaN keeps its NaN
+      const float a = rc[h] == -INFINITY ? 0.f : ex2(rc[h] - M);
+      const float4 o = *reinterpret_cast<const float4*>(rc + 16 + h * D + d4);
+      num.x = fmaf(a, o.x, num.x);
+      num.y = fmaf(a, o.y, num.y);
+      num.z = fmaf(a, o.z, num.z);
+      num.w = fmaf(a, o.w, num.w);
+      den = fmaf(a, rc[8 + h], den);
+    }
+    const long long f = pair_first(p);
+    if (f >= s0 && f + pair_len(p) <= s1) {
+      store4(O + ((int64_t)(p / Hkv) * Hq + (p % Hkv) * G + h) * D + d4, num,
+             den == 0.f ? 0.f : 1.f / den);
+    } else {
+      float* part = ws_part + ((size_t)blockIdx.x * 2 + (f < s0 ? 0 : 1)) * rec_g;
+      *reinterpret_cast<float4*>(part + h * D + d4) = num;
+      if (d4 == 0) {
+        part[G * D + h] = M;
+        part[G * D + 8 + h] = den;
+      }
+    }
+  }
+  // ---- pairs split between blocks: the last block to arrive joins the records.
+  // Only the block's first and last group can be such.
+  __threadfence();
+  __syncthreads();
+  auto block_of = [&](long long s) { return (int)(((s + 1) * grid + total - 1) / total - 1); };
+  if (t < 2) {
+    s_last[t] = -1;
+    if (groups > t) {
+      const int p = s_gpair[t == 0 ? 0 : groups - 1];
+      const long long f = pair_first(p), e = f + pair_len(p);
+      if (f < s0 || e > s1) {
+        const int parts = block_of(e - 1) - block_of(f) + 1;
+        if (atomicAdd(&ws_ctr[p], 1) == parts - 1) s_last[t] = p;
+      }
+    }
+  }
+  __syncthreads();
+  for (int k = 0; k < 2; ++k) {
+    const int p = s_last[k];
+    if (p < 0) continue;
+    __threadfence();
+    const long long f = pair_first(p);
+    const int xf = block_of(f), parts = block_of(f + pair_len(p) - 1) - xf + 1;
+    // the pair is the last of its first block and the first of the others
+    auto record = [&](int x) { return ws_part + ((size_t)(xf + x) * 2 + (x == 0 ? 1 : 0)) * rec_g; };
+    // Threads e + E y take the records y, y + PS, ... of the e-th float4; m and l
+    // of all records and the threads' sums go through the warps' records' room.
+    float2* ml = reinterpret_cast<float2*>(rec0);                  // [parts][8]
+    float* sums = rec0 + 2 * 8 * kQGridMax;                        // [PS][E][8]
+    const int PS = min(kQThreads / E, kJoinSums / E);
+    const int e = t % E, y = t / E, h = e / (D / 4), d4 = (e - h * (D / 4)) * 4;
+    constexpr int U = 4;
+    float4 pre[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (y < PS && y + u * PS < parts)
+        pre[u] = __ldcg(reinterpret_cast<const float4*>(record(y + u * PS) + h * D + d4));
+    for (int i = t; i < parts * G; i += kQThreads) {
+      const float* r = record(i / G) + G * D + i % G;
+      ml[i / G * 8 + i % G] = make_float2(__ldcg(r), __ldcg(r + 8));
+    }
+    __syncthreads();
+    float num[4] = {0.f, 0.f, 0.f, 0.f}, den = 0.f;
+    if (y < PS) {
+      float M = -INFINITY;
+#pragma unroll 8
+      for (int x = 0; x < parts; ++x) M = fmaxf(M, ml[x * 8 + h].x);
+      auto add = [&](int x, const float4& o) {
+        const float2 w = ml[x * 8 + h];
+        const float a = w.x == -INFINITY ? 0.f : ex2(w.x - M);
+        num[0] = fmaf(a, o.x, num[0]);
+        num[1] = fmaf(a, o.y, num[1]);
+        num[2] = fmaf(a, o.z, num[2]);
+        num[3] = fmaf(a, o.w, num[3]);
+        den = fmaf(a, w.y, den);
+      };
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (y + u * PS < parts) add(y + u * PS, pre[u]);
+#pragma unroll 4
+      for (int x = y + U * PS; x < parts; x += PS)
+        add(x, __ldcg(reinterpret_cast<const float4*>(record(x) + h * D + d4)));
+      if (y > 0) {
+        float* sm = sums + ((y - 1) * E + e) * 8;
+        *reinterpret_cast<float4*>(sm) = make_float4(num[0], num[1], num[2], num[3]);
+        sm[4] = den;
+      }
+    }
+    __syncthreads();
+    if (y == 0) {
+      for (int z = 1; z < PS; ++z) {
+        const float* sm = sums + ((z - 1) * E + e) * 8;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) num[i] += sm[i];
+        den += sm[4];
+      }
+      store4(O + ((int64_t)(p / Hkv) * Hq + (p % Hkv) * G + h) * D + d4,
+             make_float4(num[0], num[1], num[2], num[3]), den == 0.f ? 0.f : 1.f / den);
+    }
+    __syncthreads();
+  }
 }
 
 Q8Plan plan_q8(int batch, int Hq, int Hkv, int d, int topk, int max_blocks) {
@@ -559,7 +793,7 @@ Q8Plan plan_q8(int batch, int Hq, int Hkv, int d, int topk, int max_blocks) {
   p.off_off = up(lists);
   p.off_ctr = up(p.off_off + ((size_t)batch + 1) * sizeof(int32_t));
   p.off_part = up(p.off_ctr + pairs * sizeof(int));
-  p.bytes = up(p.off_part + (size_t)kQGridMax * 2 * (Hq / Hkv) * (d + 2) * sizeof(float));
+  p.bytes = up(p.off_part + (size_t)kQGridMax * 2 * ((size_t)(Hq / Hkv) * d + 16) * sizeof(float));
   return p;
 }
 
@@ -584,9 +818,8 @@ static cudaError_t launch_q8_t(const Q8Plan& p, const void* q, const void* Kp, c
       ws_idx, ws_ctr, ws_off, (T*)O, idx_out, 1.0f / sqrtf((float)D));
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  const int stages = D == 128 ? 3 : 8;
-  const size_t smem2 = (size_t)(D / 16) * 32 * 16 + 8 * sizeof(float) +
-                       (size_t)kQW * 8 * (D + 2) * sizeof(float) +
+  constexpr int stages = q8_stages(D);
+  const size_t smem2 = (size_t)kQW * 8 * (D + 2) * sizeof(float) +
                        (size_t)kQW * 8 * sizeof(float4) +
                        (size_t)kQW * stages * 2 * kSlice * D;
   int dev = 0, sms = 0;
@@ -598,11 +831,21 @@ static cudaError_t launch_q8_t(const Q8Plan& p, const void* q, const void* Kp, c
   e = cudaFuncSetAttribute(q8_split_kernel<T, D, F>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            (int)smem2);
   if (e != cudaSuccess) return e;
-  q8_split_kernel<T, D, F><<<grid, kQThreads, smem2, st>>>(
-      (const T*)q, (const uint8_t*)Kp, Ks, (const uint8_t*)Vp, Vs, table, seqlens, batch, Hq, Hkv,
-      B, max_blocks, num_pages, p.kk, p.width, stages, kQW, ws_idx, ws_off, ws_part, ws_ctr,
-      (T*)O, scale * 1.4426950408889634f);
-  return cudaGetLastError();
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(kQThreads);
+  cfg.dynamicSmemBytes = smem2;
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, q8_split_kernel<T, D, F>, (const T*)q, (const uint8_t*)Kp, Ks,
+                            (const uint8_t*)Vp, Vs, table, seqlens, batch, Hq, Hkv, B, max_blocks,
+                            num_pages, p.kk, p.width, kQW, (const int32_t*)ws_idx,
+                            (const int32_t*)ws_off, ws_part, ws_ctr, (T*)O,
+                            scale * 1.4426950408889634f);
 }
 
 cudaError_t launch_decode_q8(const Q8Plan& p, const void* q, const void* Kp, const float* Ks,
