@@ -83,6 +83,15 @@ __device__ __forceinline__ uint32_t lanemask_lt() {
   return m;
 }
 
+// Cluster barrier: shared-memory and global writes before the arrival are visible behind
+// the wait.
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 // Capacity of the candidate list that warp_select_topk may use to filter a
 // long row before its radix passes.
 constexpr int kSelCap = 256;

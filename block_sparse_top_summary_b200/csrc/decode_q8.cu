@@ -166,19 +166,110 @@ __device__ __forceinline__ int tile_at(int r, int c) {
 }  // namespace
 
 // ---------------------------------------------------------------- 1. route
+namespace {
+
+constexpr int kListCap = 512;  // candidates that the quick selection can list
+
+// v to the same shared word of the cluster's first block.
+__device__ __forceinline__ void st_first(float* p, float v) {
+  uint32_t a = (uint32_t)__cvta_generic_to_shared(p), r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(a));
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(r), "f"(v) : "memory");
+}
+
+// Entries of keys[0 .. n) (n up to a multiple of 4, the rest 0) that come before key
+// at position i: the larger ones, and the equal ones of a lower position.
+__device__ __forceinline__ int rank_of(const uint32_t* keys, int n, uint32_t key, int i) {
+  int r = 0;
+#pragma unroll 4
+  for (int u = 0; u < n; u += 4) {
+    const uint4 k = *reinterpret_cast<const uint4*>(keys + u);
+    r += (k.x > key || (k.x == key && u < i)) + (k.y > key || (k.y == key && u + 1 < i)) +
+         (k.z > key || (k.z == key && u + 2 < i)) + (k.w > key || (k.w == key && u + 3 < i));
+  }
+  return r;
+}
+
+// block_select_topk with few passes over the scores, for k <= 256.  Each of the
+// 256 threads takes the largest of its candidates; the k-th largest of these, T, is not
+// above the k-th largest score, so whatever is selected is >= T.  The candidates
+// >= T, in index order, are few (about k plus the doubles), and each counts those
+// before it.  A list longer than kListCap (many equal scores) is left to
+// block_select_topk.  2046 candidates, k = 32: 2 us against 6.
+// keys: 256 + kListCap words, list: kListCap entries of shared memory.
+__device__ int block_select_quick(const float* sc, int n, int k, int first, int32_t* out,
+                                  uint32_t* keys, uint16_t* list, uint32_t* hist, int* sbuf) {
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  if (k <= 0 || k > 256 || k >= n) return block_select_topk(sc, n, k, first, out, hist, sbuf);
+  uint32_t best = 0;
+  for (int e = t; e < n; e += 256) best = max(best, order_key(sc[e]));
+  keys[t] = best;
+  __syncthreads();
+  if (rank_of(keys, 256, best, t) == k - 1) sbuf[8] = (int)best;
+  __syncthreads();
+  const uint32_t T = (uint32_t)sbuf[8];
+  // a warp lists a contiguous run
+  const int seg = ((n + 255) / 256) * 32, e0 = warp * seg, e1 = min(e0 + seg, n);
+  int c = 0;
+  for (int e = e0 + lane; e - lane < e1; e += 32)
+    c += __popc(__ballot_sync(0xffffffffu, e < e1 && order_key(sc[e]) >= T));
+  if (lane == 0) sbuf[warp] = c;
+  __syncthreads();
+  int pos = 0, m = 0;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) {
+    if (w < warp) pos += sbuf[w];
+    m += sbuf[w];
+  }
+  if (m > kListCap) {
+    __syncthreads();
+    return block_select_topk(sc, n, k, first, out, hist, sbuf);
+  }
+  uint32_t* lk = keys + 256;
+  for (int e = e0 + lane; e - lane < e1; e += 32) {
+    const uint32_t key = e < e1 ? order_key(sc[e]) : 0u;
+    const bool in = e < e1 && key >= T;
+    const uint32_t mask = __ballot_sync(0xffffffffu, in);
+    if (in) {
+      const int at = pos + __popc(mask & lanemask_lt());
+      list[at] = (uint16_t)e;
+      lk[at] = key;
+    }
+    pos += __popc(mask);
+  }
+  if (t < 4 && m + t < kListCap) lk[m + t] = 0;  // up to a multiple of 4
+  __syncthreads();
+  int done = 0;
+  for (int i0 = 0; i0 < m; i0 += 256) {
+    const int i = i0 + t;
+    const bool take = i < m && rank_of(lk, m, lk[i], i) < k;
+    int tot;
+    const int at = block_excl_scan(take ? 1 : 0, sbuf, &tot);
+    if (take) out[done + at] = first + (int)list[i];
+    done += tot;
+  }
+  return k;
+}
+
+}  // namespace
+
+// One cluster of CS blocks a (sequence, KV head); each scores a share of the
+// candidates into the first block's shared memory, which then selects.  The last
+// cluster sums the slices of the batch.
 template <typename T, int D>
 __global__ void __launch_bounds__(256, 2) q8_route_kernel(
     const T* __restrict__ q, const float* __restrict__ S, const int32_t* __restrict__ seqlens,
-    int batch, int Hq, int Hkv, int Lmax, int B, int nsum, int kk, int width,
+    int batch, int Hq, int Hkv, int Lmax, int B, int nsum, int kk, int width, int CS,
     int32_t* __restrict__ ws_idx, int* __restrict__ ws_ctr, int32_t* __restrict__ ws_off,
     T* __restrict__ O, int32_t* __restrict__ idx_out, float inv_sqrt_d) {
   constexpr int SL = D / 32;
   extern __shared__ __align__(16) float smem[];
   __shared__ int sbuf[16];
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-  const int bg = blockIdx.x;
+  const int bg = blockIdx.x / CS, rank = blockIdx.x - bg * CS;
   grid_launch_next();  // the split kernel's blocks may come in as these leave
   if (bg == batch * Hkv) {
+    if (rank > 0) return;
     // slices of the sequences before each, per KV head
     int base = 0;
     for (int b0 = 0; b0 < batch; b0 += 256) {
@@ -191,16 +282,17 @@ __global__ void __launch_bounds__(256, 2) q8_route_kernel(
     if (t == 0) ws_off[batch] = base;
     return;
   }
-  if (t == 0) ws_ctr[bg] = 0;
+  if (t == 0 && rank == 0) ws_ctr[bg] = 0;
   const int b = bg / Hkv, g = bg - (bg / Hkv) * Hkv, G = Hq / Hkv;
   const int L = seqlens[b];
   const bool valid = L >= 1 && L <= Lmax;
   const int last = valid ? (L - 1) / B : 0;
   const int n = valid ? max(last - 1, 0) : 0;  // candidates 1 .. last - 1
-  if (!valid) {  // no slices: nothing else writes these rows
-    for (int e = t; e < G * D; e += 256) store_out(O + ((int64_t)b * Hq + g * G) * D + e, 0.f);
-  }
   if (n <= kk) {
+    if (rank > 0) return;
+    if (!valid) {  // no slices: nothing else writes these rows
+      for (int e = t; e < G * D; e += 256) store_out(O + ((int64_t)b * Hq + g * G) * D + e, 0.f);
+    }
     // every block: the list is 0 .. last, and the split pass knows it
     if (idx_out != nullptr) {
       const int c = valid ? last + 1 : 0;
@@ -208,9 +300,12 @@ __global__ void __launch_bounds__(256, 2) q8_route_kernel(
     }
     return;
   }
-  float* qb = smem;                                      // [D]
-  uint32_t* hist = reinterpret_cast<uint32_t*>(qb + D);  // [256]
-  float* sc = reinterpret_cast<float*>(hist + 256);      // [nsum]
+  cluster_arrive();  // every block of the cluster has begun
+  float* qb = smem;                                                  // [D]
+  uint32_t* hist = reinterpret_cast<uint32_t*>(qb + D);              // [256]
+  uint32_t* keys = hist + 256;                                       // [256 + kListCap]
+  uint16_t* list = reinterpret_cast<uint16_t*>(keys + 256 + kListCap);  // [kListCap]
+  float* sc = reinterpret_cast<float*>(list + kListCap);             // [nsum]
   if (t < D) {
     float s = 0.f;
     for (int h = 0; h < G; ++h) s += (float)q[((int64_t)b * Hq + g * G + h) * D + t];
@@ -220,8 +315,10 @@ __global__ void __launch_bounds__(256, 2) q8_route_kernel(
   float qs[SL];
 #pragma unroll
   for (int e = 0; e < SL; ++e) qs[e] = qb[lane * SL + e];
+  cluster_wait();
   const float* Sg = S + ((int64_t)b * Hkv + g) * nsum * D + lane * SL;
-  for (int j0 = 1 + warp * 32; j0 <= n; j0 += 32 * 8) {
+  // steps of 32 candidates, dealt to the warps of all blocks
+  for (int j0 = 1 + (rank * 8 + warp) * 32; j0 <= n; j0 += 32 * 8 * CS) {
     float v[32];
 #pragma unroll
     for (int c = 0; c < 32; ++c) {
@@ -232,18 +329,20 @@ __global__ void __launch_bounds__(256, 2) q8_route_kernel(
         x[0] = y.x; x[1] = y.y; x[2 % SL] = y.z; x[3 % SL] = y.w;
       } else {
         const float2 y = __ldg(reinterpret_cast<const float2*>(Sg + (int64_t)j * D));
-        x[0] = y.x; x[1 % SL] = y.y;
+        x[0] = y.x; x[1] = y.y;
       }
 #pragma unroll
       for (int e = 0; e < SL; ++e) a = fmaf(x[e], qs[e], a);
       v[c] = a;
     }
     const float dot = reduce32_transpose(v);
-    if (j0 + lane <= n) sc[j0 + lane - 1] = dot * inv_sqrt_d;
+    if (j0 + lane <= n) st_first(sc + j0 + lane - 1, dot * inv_sqrt_d);
   }
-  __syncthreads();
+  cluster_arrive();
+  cluster_wait();
+  if (rank > 0) return;
   int32_t* row = ws_idx + (int64_t)bg * width;
-  block_select_topk(sc, n, kk, 1, row + 1, hist, sbuf);
+  block_select_quick(sc, n, kk, 1, row + 1, keys, list, hist, sbuf);
   if (t == 0) {
     row[0] = 0;
     row[kk + 1] = last;
@@ -809,38 +908,50 @@ static cudaError_t launch_q8_t(const Q8Plan& p, const void* q, const void* Kp, c
   int32_t* ws_off = reinterpret_cast<int32_t*>(w + p.off_off);
   int* ws_ctr = reinterpret_cast<int*>(w + p.off_ctr);
   float* ws_part = reinterpret_cast<float*>(w + p.off_part);
-  const size_t smem1 = sizeof(float) * (D + 256 + (size_t)max_blocks);
-  cudaError_t e = cudaFuncSetAttribute(q8_route_kernel<T, D>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem1);
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  q8_route_kernel<T, D><<<batch * Hkv + 1, 256, smem1, st>>>(
-      (const T*)q, S, seqlens, batch, Hq, Hkv, max_blocks * B, B, max_blocks, p.kk, p.width,
-      ws_idx, ws_ctr, ws_off, (T*)O, idx_out, 1.0f / sqrtf((float)D));
-  e = cudaGetLastError();
+  e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  // Few pairs of long rows: several blocks score a pair's summaries, as many as
+  // the GPU takes at once (2 an SM) and as leave each warp a step of 32.
+  int CS = 1;
+  while (CS < 8 && batch * (long long)Hkv * CS * 2 <= 2 * sms && max_blocks >= CS * 2 * 256) CS *= 2;
+  const size_t smem1 = sizeof(float) * (D + 512 + kListCap + kListCap / 2 + (size_t)max_blocks);
+  if (smem1 > 47 * 1024) {  // the static arrays count too
+    e = cudaFuncSetAttribute(q8_route_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)smem1);
+    if (e != cudaSuccess) return e;
+  }
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = CS;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(batch * Hkv + 1) * CS);
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = smem1;
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, q8_route_kernel<T, D>, (const T*)q, S, seqlens, batch, Hq, Hkv,
+                         max_blocks * B, B, max_blocks, p.kk, p.width, CS, ws_idx, ws_ctr, ws_off,
+                         (T*)O, idx_out, 1.0f / sqrtf((float)D));
   if (e != cudaSuccess) return e;
   constexpr int stages = q8_stages(D);
   const size_t smem2 = (size_t)kQW * 8 * (D + 2) * sizeof(float) +
                        (size_t)kQW * 8 * sizeof(float4) +
                        (size_t)kQW * stages * 2 * kSlice * D;
-  int dev = 0, sms = 0;
-  e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e != cudaSuccess) return e;
   const int grid = sms < kQGridMax ? sms : kQGridMax;
   e = cudaFuncSetAttribute(q8_split_kernel<T, D, F>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            (int)smem2);
   if (e != cudaSuccess) return e;
-  cudaLaunchAttribute attr{};
+  attr = cudaLaunchAttribute{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3(kQThreads);
   cfg.dynamicSmemBytes = smem2;
-  cfg.stream = st;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, q8_split_kernel<T, D, F>, (const T*)q, (const uint8_t*)Kp, Ks,
                             (const uint8_t*)Vp, Vs, table, seqlens, batch, Hq, Hkv, B, max_blocks,
                             num_pages, p.kk, p.width, kQW, (const int32_t*)ws_idx,

@@ -120,6 +120,35 @@ def test_plan_lengths_out_of_range_and_sums_past_31_bits(ssa):
     _check_plan(ssa, (have, want[::-1].copy(), None, big, np.arange(50), [3, 20]), 128, 1000)
 
 
+def test_tensors_of_another_kind_are_refused(ssa):
+    B, d, L = 16, 64, [20]
+    cache = _cache("i8", d, B, 2, L, seed=30)
+    K, Ks, V, Vs, S = (x.to(DEV) for x in cache[:5])
+    table, lens = _dev(cache[5]), _dev(np.asarray(L))
+    q = torch.randn(1, 4, d, device=DEV)
+
+    def call(q=q, K=K, Ks=Ks, V=V, S=S, table=table, lens=lens, **kw):
+        return ssa.ssa_decode_paged_q8(q, K, Ks, V, Vs, S, table, lens, B, 1 << 20, **kw)
+
+    call()
+    for bad in (dict(q=q.cpu()), dict(table=table.cpu()), dict(S=S[:, :1]), dict(lens=lens[:0]),
+                dict(K=K.transpose(0, 1)), dict(q=q.transpose(1, 2)), dict(Ks=Ks[:, :1])):
+        with pytest.raises(ValueError):
+            call(**bad)
+    for bad in (dict(q=q.half()), dict(table=table.long()), dict(V=V.view(torch.uint8)),
+                dict(K=K.view(torch.uint8)), dict(Ks=Ks.double()), dict(O=torch.empty_like(q).bfloat16())):
+        with pytest.raises(TypeError):
+            call(**bad)
+    with pytest.raises(ssa.SSAError):
+        call(workspace=torch.empty(64, dtype=torch.uint8, device=DEV))
+    with pytest.raises(ssa.SSAError):  # no summaries, and blocks to choose from
+        ssa.ssa_decode_paged_q8(q, K, Ks, V, Vs, None, torch.zeros(1, 9, dtype=torch.int32,
+                                                                   device=DEV), lens, B, 2)
+    with pytest.raises(TypeError):
+        ssa.ssa_page_plan(lens.long(), lens, table, lens, lens, B, 4)
+    torch.cuda.synchronize()
+
+
 def test_plan_bad_pool_state_stays_in_bounds(ssa):
     # a head or a count outside the ring: clamped; a page that comes back when
     # the ring is full: dropped
@@ -419,6 +448,22 @@ def test_decode_long_rows_and_many_rows(ssa, fmt, dtype, d, n, L, B, topk):
     q = torch.randn(n, 4, d, generator=torch.Generator().manual_seed(2)).to(TORCH[dtype])
     got, idx = _run_decode(ssa, cache, q, lens, B, topk)
     _check_decode(cache, q, lens, B, topk, got, idx, dtype)
+
+
+@pytest.mark.parametrize("topk", [1, 31, 200, 256, 257, 900])
+@pytest.mark.parametrize("ties", [False, True])
+def test_decode_selection_of_long_rows(ssa, topk, ties):
+    # up to 1100 candidates; with ties, few distinct scores: lists longer than the
+    # quick selection holds, and equal scores go to the lower block
+    B, d, L = 16, 64, [16 * 1102, 16 * 260 + 3, 16 * 1000]
+    cache = list(_cache("i8", d, B, 2, L, seed=20))
+    q = torch.randn(3, 4, d, generator=torch.Generator().manual_seed(21))
+    if ties:
+        few = torch.randn(3, 2, 5, d, generator=torch.Generator().manual_seed(22))
+        which = torch.randint(0, 5, cache[4].shape[:3], generator=torch.Generator().manual_seed(23))
+        cache[4] = torch.gather(few, 2, which[..., None].expand(*which.shape, d)).contiguous()
+    got, idx = _run_decode(ssa, cache, q, L, B, topk)
+    _check_decode(cache, q, L, B, topk, got, idx, "f32")
 
 
 def test_decode_scale_argument_loud_caches_and_quiet_queries(ssa):
