@@ -414,7 +414,8 @@ ssa_status ssa_page_plan(const int32_t* have, const int32_t* want, const int32_t
                          int32_t* slots, int max_new, ssa_stream stream) {
   if (batch <= 0 || B <= 0 || max_blocks <= 0 || num_pages <= 0 || max_new < 0)
     return SSA_ERR_INVALID_ARG;
-  if (B % 16 != 0 || B > 128 || batch > ssa::kPlanMaxBatch) return SSA_ERR_UNSUPPORTED;
+  if (B % 16 != 0 || B > 128 || batch > ssa::kPlanMaxBatch || max_new > 1 << 30)
+    return SSA_ERR_UNSUPPORTED;
   if ((long long)max_blocks * B > 0x7fffffffLL || (long long)num_pages * B > 0x7fffffffLL)
     return SSA_ERR_UNSUPPORTED;
   if (have == nullptr || want == nullptr || page_table == nullptr || ring == nullptr ||

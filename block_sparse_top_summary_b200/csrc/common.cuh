@@ -83,6 +83,13 @@ __device__ __forceinline__ uint32_t lanemask_lt() {
   return m;
 }
 
+// Programmatic dependent launch: a kernel lets the next one of its stream start, and
+// that one waits here until the first has ended and its writes are visible.
+__device__ __forceinline__ void grid_launch_next() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // Cluster barrier: shared-memory and global writes before the arrival are visible behind
 // the wait.
 __device__ __forceinline__ void cluster_arrive() {

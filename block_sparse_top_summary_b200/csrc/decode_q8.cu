@@ -123,13 +123,6 @@ __device__ __forceinline__ void split_half2(float a, float b, uint32_t& hi, uint
   lo = half2_bits(a - f.x, b - f.y);
 }
 
-// Programmatic dependent launch: a kernel lets the next one of its stream start, and
-// that one waits here until the first has ended and its writes are visible.
-__device__ __forceinline__ void grid_launch_next() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 // Four outputs v * f on end.
 __device__ __forceinline__ void store4(float* p, float4 v, float f) {
   *reinterpret_cast<float4*>(p) = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);

@@ -32,6 +32,22 @@ struct PlanRow {
   long long n, need, back;
 };
 
+// x / B for 0 <= x < 2^31, B = 16 d with d <= 8: with m = floor(2^32 / d) + 1 and
+// n = x / 16 < 2^27, n m / 2^32 is less than n d / 2^32 < 1 / d above n / d.
+struct BlockDiv {
+  int B;
+  uint32_t m;
+  __device__ explicit BlockDiv(int B_) : B(B_), m(B_ > 16 ? 0xffffffffu / (B_ / 16) + 1 : 0) {}
+  __device__ int operator()(int x) const {
+    const uint32_t n = (uint32_t)x >> 4;
+    return m != 0 ? (int)__umulhi(n, m) : (int)n;
+  }
+  __device__ int up(int x) const {  // blocks of x tokens
+    const int q = (*this)(x);
+    return q + (q * B < x ? 1 : 0);
+  }
+};
+
 // Exclusive prefix sums of three values a thread; total: their sums.
 __device__ __forceinline__ PlanRow plan_scan(PlanRow v, PlanRow* wsum, PlanRow* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -87,12 +103,34 @@ __device__ __forceinline__ int row_above(const int* incl, int n, int x) {
   return lo;
 }
 
+// The same for one x by a whole warp, 32 guesses a step, among the n rows from lo on.
+__device__ __forceinline__ int find_row(const int* incl, int lo, int n, int x) {
+  const int lane = threadIdx.x & 31;
+  while (n > 1) {
+    const int step = (n + 31) / 32;
+    const int i = lo + min((lane + 1) * step, n) - 1;
+    const int k = __ffs(__ballot_sync(0xffffffffu, incl[i] > x)) - 1;
+    lo += k * step;
+    n = min(step, n - k * step);
+  }
+  return lo;
+}
+
+// row_above for an x of each lane, first <= x <= last.
+__device__ __forceinline__ int row_above_warp(const int* incl, int n, int x, int first, int last) {
+  const int lo = find_row(incl, 0, n, first);
+  if (incl[lo] > last) return lo;
+  const int hi = find_row(incl, lo, n - lo, last);
+  return lo + row_above(incl + lo, hi - lo + 1, x);
+}
+
 __device__ __forceinline__ int clamp_int(long long v) { return v > kIntMax ? kIntMax : (int)v; }
 
 }  // namespace
 
-// V: tokens on end that a thread places at a time (1 or 8).
-template <int V>
+// kSlots: one block, which fills the slots; else a cluster, which writes the first
+// slot of each row, and page_slots_kernel follows.
+template <bool kSlots>
 __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(
     const int32_t* have, const int32_t* want, const int32_t* keep, int batch, int B,
     int32_t* __restrict__ table, int max_blocks, int num_pages, int32_t* __restrict__ ring,
@@ -109,7 +147,9 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(
   __shared__ int s_taken;
   const int t = threadIdx.x;
   const int blocks = gridDim.x, rank = blockIdx.x;  // one cluster
+  if (!kSlots) grid_launch_next();
   const int cap = max_blocks * B;
+  const BlockDiv div(B);
   // a pool state out of range is taken as an empty or a full ring
   const int head = min(max(pool[0], 0), num_pages - 1);
   const int count = min(max(pool[1], 0), num_pages);
@@ -128,7 +168,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(
       r.w = -1;
       return r;
     }
-    const int hb = (r.h + B - 1) / B, wb = (r.w + B - 1) / B;
+    const int hb = div.up(r.h), wb = div.up(r.w);
     if (r.w >= r.h) {
       r.v.n = r.w - r.h;
       r.v.need = wb - hb;
@@ -171,86 +211,60 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(
   taken = s_taken;  // the rows that take pages are a prefix of those that ask
   const int tokens = (int)min(total.n, (long long)max_new);
   const int given = (int)min(total.back, (long long)(num_pages - count));
-  if (blocks > 1) cluster_arrive();  // this block has read the lengths and the pool's state
+  if (!kSlots) cluster_arrive();  // this block has read the lengths and the pool's state
 
   // entry i behind the head; i <= num_pages
   auto ring_at = [&](int i) {
     const int x = head + i;
     return x >= num_pages ? x - num_pages : x;
   };
-  for (int i0 = (rank * kPlanThreads + t) * V; i0 < max_new; i0 += blocks * kPlanThreads * V) {
-    // first where each token's page stands, then the pages, all at once
-    const int32_t* at[V];
-    int r[V];
-    int b = 0, end = 0, j = 0, hb = 0, place = 0;
-    const int32_t* word = nullptr;
-    auto enter = [&](int i) {  // token i of row b
-      end = tok[b];
-      const int x = row[b], h = x & kIntMax;
-      const int pos = h + i - (b > 0 ? tok[b - 1] : 0);
-      hb = x < 0 ? (h + B - 1) / B : -1;  // -1: a refused row
-      j = pos / B;
-      place = pos - j * B;
-    };
-    auto find = [&]() {  // block j of row b, of which the call may add some
-      word = hb < 0    ? nullptr
-             : j < hb ? table + (int64_t)b * max_blocks + j
-                      : ring + ring_at((b > 0 ? pag[b - 1] : 0) + (j - hb));
-    };
-    if (i0 < tokens) {
-      b = row_above(tok, batch, i0);
-      enter(i0);
-      find();
-    }
-#pragma unroll
-    for (int u = 0; u < V; ++u) {
-      if (u > 0 && i0 + u < tokens) {
-        ++place;
-        if (i0 + u >= end) {
-          do ++b; while (tok[b] <= i0 + u);
-          enter(i0 + u);
-          find();
-        } else if (place == B) {
-          ++j;
-          place = 0;
-          find();
-        }
+  const int lane = t & 31;
+  // slot of token i of row b, which holds x (bit 31: it grows); the call may add pages
+  auto slot_at = [&](int b, int x, int i) {
+    if (x >= 0) return -1;
+    const int h = x & kIntMax;
+    const int pos = h + i - (b > 0 ? tok[b - 1] : 0);
+    const int j = div(pos), hb = div.up(h);
+    const int page = j < hb ? table[(int64_t)b * max_blocks + j]
+                            : ring[ring_at((b > 0 ? pag[b - 1] : 0) + (j - hb))];
+    return page >= 0 && page < num_pages ? page * B + pos - j * B : -1;
+  };
+  if constexpr (kSlots) {
+    for (int w0 = t - lane; w0 < max_new; w0 += kPlanThreads) {
+      const int i = w0 + lane;
+      int slot = -1;
+      if (w0 < tokens) {
+        const int last = min(w0 + 32, tokens) - 1;
+        const int b = row_above_warp(tok, batch, min(i, last), w0, last);
+        if (i < tokens) slot = slot_at(b, row[b], i);
       }
-      at[u] = i0 + u < tokens ? word : nullptr;
-      r[u] = place;
+      if (i < max_new) slots[i] = slot;
     }
-    int out[V];
-#pragma unroll
-    for (int u = 0; u < V; ++u) out[u] = at[u] != nullptr ? *at[u] : -1;
-#pragma unroll
-    for (int u = 0; u < V; ++u)
-      out[u] = out[u] >= 0 && out[u] < num_pages ? out[u] * B + r[u] : -1;
-    if (V == 8 && i0 + V <= max_new) {
-      *reinterpret_cast<int4*>(slots + i0) =
-          make_int4(out[0], out[1 % V], out[2 % V], out[3 % V]);
-      *reinterpret_cast<int4*>(slots + i0 + 4) =
-          make_int4(out[4 % V], out[5 % V], out[6 % V], out[7 % V]);
-    } else {
-#pragma unroll
-      for (int u = 0; u < V; ++u)
-        if (i0 + u < max_new) slots[i0 + u] = out[u];
+  } else {
+    // the first of each row: whether it is granted, for page_slots_kernel
+    for (int b = rank * kPlanThreads + t; b < batch; b += blocks * kPlanThreads) {
+      const int i = b > 0 ? tok[b - 1] : 0;
+      if (tok[b] > i && i < tokens) slots[i] = slot_at(b, row[b], i);
     }
   }
   // new blocks' pages
-  for (int i = rank * kPlanThreads + t; i < taken; i += blocks * kPlanThreads) {
+  for (int w0 = rank * kPlanThreads + t - lane; w0 < taken; w0 += blocks * kPlanThreads) {
+    const int i = min(w0 + lane, taken - 1);
     const int page = ring[ring_at(i)];
-    const int b = row_above(pag, batch, i);
-    const int hb = ((row[b] & kIntMax) + B - 1) / B;
-    table[(int64_t)b * max_blocks + hb + i - (b > 0 ? pag[b - 1] : 0)] = page;
+    const int b = row_above_warp(pag, batch, i, w0, min(w0 + 32, taken) - 1);
+    const int hb = div.up(row[b] & kIntMax);
+    if (w0 + lane < taken)
+      table[(int64_t)b * max_blocks + hb + i - (b > 0 ? pag[b - 1] : 0)] = page;
   }
   // returned pages go behind the free ones; entries taken above are not reached,
   // as at most num_pages - count come back
-  for (int i = rank * kPlanThreads + t; i < given; i += blocks * kPlanThreads) {
-    const int b = row_above(bak, batch, i);
-    ring[ring_at(count + i)] =
-        table[(int64_t)b * max_blocks + from[b] + i - (b > 0 ? bak[b - 1] : 0)];
+  for (int w0 = rank * kPlanThreads + t - lane; w0 < given; w0 += blocks * kPlanThreads) {
+    const int i = min(w0 + lane, given - 1);
+    const int b = row_above_warp(bak, batch, i, w0, min(w0 + 32, given) - 1);
+    const int page = table[(int64_t)b * max_blocks + from[b] + i - (b > 0 ? bak[b - 1] : 0)];
+    if (w0 + lane < given) ring[ring_at(count + i)] = page;
   }
-  if (blocks > 1) cluster_wait();
+  if (!kSlots) cluster_wait();
   if (rank > 0) return;
   for (int b = r0; b < r1; ++b) got[b] = len[b];
   if (t == 0) {
@@ -260,15 +274,72 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(
   }
 }
 
+// The slots of granted rows from what page_plan_kernel has written: lengths, prefix
+// sums, page table and the first slot of each row (-1: refused).  Another warp may be
+// writing that one again, with the same value.  A warp takes 256 slots on end.
+__global__ void __launch_bounds__(256) page_slots_kernel(const int32_t* __restrict__ got,
+                                                         const int32_t* __restrict__ cu,
+                                                         const int32_t* __restrict__ table,
+                                                         int batch, int B, int max_blocks,
+                                                         int num_pages, int32_t* slots,
+                                                         int max_new) {
+  const int lane = threadIdx.x & 31;
+  const int w0 = (blockIdx.x * 8 + (threadIdx.x >> 5)) * 256;
+  const BlockDiv div(B);
+  grid_wait();
+  const int tokens = cu[batch];
+  if (w0 >= max_new) return;
+  const int last = min(w0 + 256, tokens) - 1;
+  int lo = 0, hi = 0;
+  if (w0 < tokens) {
+    lo = find_row(cu + 1, 0, batch, w0);
+    hi = cu[lo + 1] > last ? lo : find_row(cu + 1, lo, batch - lo, last);
+  }
+  auto slot_of = [&](int page, int r) {
+    return page >= 0 && page < num_pages ? page * B + r : -1;
+  };
+  if (lo == hi && last == w0 + 255) {
+    // one row: 8 slots on end a thread, in at most two blocks (B >= 16)
+    const int c = cu[lo], p0 = got[lo] - (cu[lo + 1] - c), i0 = w0 + lane * 8;
+    int out[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) out[u] = -1;
+    if (slots[c] >= 0) {
+      const int pos = p0 + i0 - c, j = div(pos), r = pos - j * B, left = B - r;
+      const int32_t* w = table + (int64_t)lo * max_blocks + j;
+      const int a = w[0], z = left < 8 ? w[1] : a;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) out[u] = u < left ? slot_of(a, r + u) : slot_of(z, u - left);
+    }
+    *reinterpret_cast<int4*>(slots + i0) = make_int4(out[0], out[1], out[2], out[3]);
+    *reinterpret_cast<int4*>(slots + i0 + 4) = make_int4(out[4], out[5], out[6], out[7]);
+    return;
+  }
+#pragma unroll 4
+  for (int u = 0; u < 8; ++u) {
+    const int i = w0 + 32 * u + lane;
+    int slot = -1;
+    if (i < tokens) {
+      const int b = lo + row_above(cu + 1 + lo, hi - lo + 1, i);
+      const int c = cu[b];
+      if (slots[c] >= 0) {
+        const int pos = got[b] - (cu[b + 1] - c) + i - c, j = div(pos);
+        slot = slot_of(table[(int64_t)b * max_blocks + j], pos - j * B);
+      }
+    }
+    if (i < max_new) slots[i] = slot;
+  }
+}
+
 cudaError_t launch_page_plan(const int32_t* have, const int32_t* want, const int32_t* keep,
                              int batch, int B, int32_t* table, int max_blocks, int num_pages,
                              int32_t* ring, const int32_t* pool, int32_t* pool_out, int32_t* got,
                              int32_t* cu, int32_t* slots, int max_new, cudaStream_t st) {
   const size_t smem = (size_t)batch * 6 * sizeof(int);
-  // Up to 8192 slots one block, a token a thread, so that the pages of one-token rows
-  // are read at once; beyond, 8 tokens a thread in a cluster of 8 blocks.
+  // Up to 8192 slots one block does it all (10 us at 8192, measured with one-token
+  // rows); beyond, a cluster of 8 for rows and pages, and a second kernel for the slots.
   const bool one = max_new <= 8 * kPlanThreads;
-  const auto kernel = one ? page_plan_kernel<1> : page_plan_kernel<8>;
+  const auto kernel = one ? page_plan_kernel<true> : page_plan_kernel<false>;
   if (smem > 46 * 1024) {  // the static arrays count too
     const cudaError_t e =
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
@@ -285,8 +356,20 @@ cudaError_t launch_page_plan(const int32_t* have, const int32_t* want, const int
   cfg.stream = st;
   cfg.attrs = &attr;
   cfg.numAttrs = one ? 0 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, have, want, keep, batch, B, table, max_blocks, num_pages,
-                            ring, pool, pool_out, got, cu, slots, max_new);
+  const cudaError_t e =
+      cudaLaunchKernelEx(&cfg, kernel, have, want, keep, batch, B, table, max_blocks, num_pages,
+                         ring, pool, pool_out, got, cu, slots, max_new);
+  if (e != cudaSuccess || one) return e;
+  attr = cudaLaunchAttribute{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3((unsigned)((max_new + 2047) / 2048));
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = 0;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, page_slots_kernel, (const int32_t*)got, (const int32_t*)cu,
+                            (const int32_t*)table, batch, B, max_blocks, num_pages, slots,
+                            max_new);
 }
 
 }  // namespace ssa

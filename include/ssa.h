@@ -440,7 +440,8 @@ ssa_status ssa_decode_append_paged(void* Kp, void* Vp, ssa_dtype dtype, float* S
  * ring: [num_pages]; pool, pool_out: [2]; cu: [batch + 1]; slots: [max_new].
  * got may be have, and pool_out may be pool; nothing else may overlap.
  * slots may be NULL when max_new is 0.  Supported: B a multiple of 16 in
- * [16, 128]; batch <= 8192; max_blocks * B and num_pages * B below 2^31.
+ * [16, 128]; batch <= 8192; max_new <= 2^30; max_blocks * B and num_pages * B
+ * below 2^31.
  * Calls on one table or ring must not overlap on the device.
  */
 ssa_status ssa_page_plan(const int32_t* have, const int32_t* want, const int32_t* keep, int batch,

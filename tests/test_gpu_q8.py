@@ -95,6 +95,18 @@ def test_plan_matches_the_oracle(ssa, n, B, mb, in_place):
         _check_plan(ssa, case, B, total + 17, in_place)
 
 
+@pytest.mark.parametrize("n,B,mb,prompt", [(40, 16, 64, 1000), (700, 48, 20, 90),
+                                           (9, 128, 40, 5000), (3000, 32, 3, 30)])
+def test_plan_of_many_tokens(ssa, n, B, mb, prompt):
+    # more than 8192 slots: a cluster, 8 tokens a thread; short and long rows, refused ones
+    for seed in range(2):
+        have, want, keep, table, ring, (head, count) = _plan_case(n, B, mb, seed + n, prompt=prompt)
+        total = int(np.maximum(want - have, 0).sum())
+        for free, room in ((count, total + 3), (count, 3 * total // 4), (count // 2, total)):
+            _check_plan(ssa, (have, want, keep, table, ring, [head, free]), B, max(room, 8193),
+                        in_place=seed == 1)
+
+
 @pytest.mark.parametrize("max_new", [0, 1, 37, 300])
 @pytest.mark.parametrize("free", [0, 1, 9])
 def test_plan_refuses_rows_beyond_pages_or_tokens(ssa, max_new, free):

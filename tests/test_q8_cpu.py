@@ -42,7 +42,7 @@ def test_page_plan_rejections(lib):
     assert call(batch=0) == 1 and call(max_blocks=0) == 1 and call(num_pages=0) == 1
     assert call(max_new=-1) == 1 and call(B=0) == 1
     assert call(B=40) == 2 and call(B=144) == 2
-    assert call(batch=8193) == 2
+    assert call(batch=8193) == 2 and call(max_new=(1 << 30) + 1) == 2
     assert call(max_blocks=1 << 26) == 2      # 2^32 tokens a row
     assert call(num_pages=1 << 26) == 2       # slots past 31 bits
 
