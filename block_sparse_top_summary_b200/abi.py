@@ -524,17 +524,16 @@ def _arg(n: str, t: torch.Tensor, dtype: torch.dtype, shape: tuple, dev: int) ->
     return t.data_ptr()
 
 
-def _launch_on(stream, dev: int, *own):
-    """The stream's handle; tensors that a call allocates stay alive for the work
-    on a stream that is not the one they were allocated on."""
+def _launch_on(stream, dev: int, own=()):
+    """The stream's handle; ``own``, tensors that the call has allocated, stay alive for
+    the work on a stream that is not the one they were allocated on."""
     if stream is None:
         return _current_stream(dev)
     if stream.device_index != dev:
         raise ValueError(f"the stream is of cuda:{stream.device_index}, "
                          f"the current device is cuda:{dev}")
     for t in own:
-        if t is not None:
-            t.record_stream(stream)
+        t.record_stream(stream)
     return stream.cuda_stream
 
 
@@ -551,25 +550,27 @@ def ssa_page_plan(have, want, page_table, ring, pool, B: int, max_new: int, keep
     i32, dev = torch.int32, _device()
     batch, max_blocks = page_table.shape
     num_pages = ring.numel()
-    rows = (batch,)
-    own = []
-    if got is None or cu is None or slots is None or pool_out is None:
-        def new(t, n):
-            if t is None:
-                t = torch.empty(n, dtype=i32, device=have.device)
-                own.append(t)
-            return t
-
-        got, cu, slots, pool_out = new(got, batch), new(cu, batch + 1), new(slots, max_new), \
-            new(pool_out, 2)
+    rows, at, own = (batch,), have.device, []
+    if got is None:
+        own.append(got := torch.empty(batch, dtype=i32, device=at))
+    if cu is None:
+        own.append(cu := torch.empty(batch + 1, dtype=i32, device=at))
+    if slots is None:
+        own.append(slots := torch.empty(max_new, dtype=i32, device=at))
+    if pool_out is None:
+        own.append(pool_out := torch.empty(2, dtype=i32, device=at))
+    if len(own) < 4:
+        _arg("got", got, i32, rows, dev)
+        _arg("cu", cu, i32, (batch + 1,), dev)
+        _arg("slots", slots, i32, (max_new,), dev)
+        _arg("pool_out", pool_out, i32, (2,), dev)
     status = load_library().ssa_page_plan(
         _arg("have", have, i32, rows, dev), _arg("want", want, i32, rows, dev),
         None if keep is None else _arg("keep", keep, i32, rows, dev), batch, B,
         _arg("page_table", page_table, i32, (batch, max_blocks), dev), max_blocks, num_pages,
         _arg("ring", ring, i32, (num_pages,), dev), _arg("pool", pool, i32, (2,), dev),
-        _arg("pool_out", pool_out, i32, (2,), dev), _arg("got", got, i32, rows, dev),
-        _arg("cu", cu, i32, (batch + 1,), dev), _arg("slots", slots, i32, (max_new,), dev), max_new,
-        _launch_on(stream, dev, *own))
+        pool_out.data_ptr(), got.data_ptr(), cu.data_ptr(), slots.data_ptr(), max_new,
+        _launch_on(stream, dev, own))
     _check("ssa_page_plan", status)
     return got, cu, slots, pool_out
 
@@ -652,27 +653,33 @@ def ssa_decode_paged_q8(q, Kp, Ks, Vp, Vs, S, page_table, seqlens, B: int, topk:
     """
     i32, dev = torch.int32, _device()
     fmt, num_pages, Hkv, d, kp, ks, vp, vs = _q8_cache(Kp, Ks, Vp, Vs, B, dev)
-    batch, Hq, _ = heads = q.shape
+    heads = q.shape
+    batch, Hq, _ = heads
     max_blocks = page_table.shape[1]
     width = (topk if topk < max_blocks else max_blocks) + 2
-    own = [None, None, None]
+    qp, own = _arg("q", q, q.dtype, (batch, Hq, d), dev), []
     if O is None:
-        own[0] = O = torch.empty(heads, dtype=q.dtype, device=q.device)
-    if idx is None and want_idx:
-        own[1] = idx = torch.empty(batch, Hkv, width, dtype=i32, device=q.device)
+        own.append(O := torch.empty_like(q))
+    else:
+        _arg("O", O, q.dtype, heads, dev)
+    if idx is not None:
+        _arg("idx", idx, i32, (batch, Hkv, width), dev)
+    elif want_idx:
+        own.append(idx := torch.empty(batch, Hkv, width, dtype=i32, device=q.device))
     if workspace is None:
-        own[2] = workspace = torch.empty(
+        own.append(workspace := torch.empty(
             ssa_decode_paged_q8_workspace_size(batch, Hq, Hkv, d, B, topk, max_blocks),
-            dtype=torch.uint8, device=q.device)
+            dtype=torch.uint8, device=q.device))
+    else:
+        _arg("workspace", workspace, torch.uint8, (workspace.numel(),), dev)
     status = load_library().ssa_decode_paged_q8(
-        _arg("q", q, q.dtype, (batch, Hq, d), dev), _dtype_code(q), kp, ks, vp, vs, fmt,
+        qp, _dtype_code(q), kp, ks, vp, vs, fmt,
         None if S is None else _arg("S", S, torch.float32, (batch, Hkv, max_blocks, d), dev),
         _arg("page_table", page_table, i32, (batch, max_blocks), dev), max_blocks, num_pages,
         _arg("seqlens", seqlens, i32, (batch,), dev), batch, Hq, Hkv, d, B, topk,
-        d ** -0.5 if scale is None else scale, _arg("O", O, q.dtype, heads, dev),
-        None if idx is None else _arg("idx", idx, i32, (batch, Hkv, width), dev),
-        _arg("workspace", workspace, torch.uint8, (workspace.numel(),), dev), workspace.numel(),
-        _launch_on(stream, dev, *own))
+        d ** -0.5 if scale is None else scale, O.data_ptr(),
+        None if idx is None else idx.data_ptr(), workspace.data_ptr(), workspace.numel(),
+        _launch_on(stream, dev, own))
     _check("ssa_decode_paged_q8", status)
     return O, idx
 
