@@ -39,7 +39,7 @@ namespace {
 constexpr int kQW = 12;                 // warps of the split kernel
 constexpr int kQThreads = 32 * kQW;
 constexpr int kSlice = 16;              // keys a slice
-constexpr int kQGridMax = 256;          // most blocks of the split grid
+constexpr int kQGridMax = 160;          // most blocks of the split grid (148 SMs, one each)
 // Slices in flight or in use a warp: 144 KB (d = 128) or 192 KB (d = 64) a block.
 __host__ __device__ constexpr int q8_stages(int d) { return d == 128 ? 3 : 8; }
 
@@ -356,7 +356,7 @@ __global__ void __launch_bounds__(kQThreads, 1) q8_split_kernel(
     const T* __restrict__ q, const uint8_t* __restrict__ Kp, const float* __restrict__ Ks,
     const uint8_t* __restrict__ Vp, const float* __restrict__ Vs,
     const int32_t* __restrict__ table, const int32_t* __restrict__ seqlens, int batch, int Hq,
-    int Hkv, int B, int max_blocks, int num_pages, int kk, int width, int min_slices,
+    int Hkv, int B, int max_blocks, int num_pages, int kk, int width, int lists, int min_slices,
     const int32_t* __restrict__ ws_idx, const int32_t* __restrict__ ws_off,
     float* __restrict__ ws_part, int* __restrict__ ws_ctr, T* __restrict__ O, float scale_log2) {
   constexpr int TILE = kSlice * D;       // bytes of K (or V) of a slice
@@ -370,9 +370,11 @@ __global__ void __launch_bounds__(kQThreads, 1) q8_split_kernel(
   constexpr float kLazy = 8.0f, kUp = 4.0f, kNear = 8.0f;
   constexpr int stages = q8_stages(D);
   static_assert(stages * 2 * TILE >= REC * 4, "a warp's ring holds its record");
-  // floats of the sums that the last block's threads exchange: [PS - 1][E][8]
-  constexpr int kJoinSums = (kQW * REC - 2 * 8 * kQGridMax) / 8;
-  static_assert(kJoinSums >= 8 * (D / 4), "one float4 of each head for one thread at least");
+  // sums that half of the last block's threads can exchange, [PS - 1][E] of 8 floats
+  constexpr int kJoinSums = kQW * REC / 2 > 2 * 8 * kQGridMax
+                                ? (kQW * REC / 2 - 2 * 8 * kQGridMax) / 8
+                                : 0;
+  static_assert(kQW * REC >= 2 * 2 * 8 * kQGridMax, "m and l of two pairs' records");
   // q in fp32 keeps a low part; bf16 is exact in f16
   constexpr bool kLow = sizeof(T) == 4;
   extern __shared__ __align__(128) unsigned char q8_smem[];
@@ -381,15 +383,43 @@ __global__ void __launch_bounds__(kQThreads, 1) q8_split_kernel(
   __shared__ int s_list[2 * kQW];            // records in use
   __shared__ int s_from[kQW + 2], s_gpair[kQW + 1];  // a group's records in s_list, its pair
   __shared__ int s_last[2];
+  __shared__ int32_t s_off[kQThreads + 1];
 
   const int G = Hq / Hkv, spb = B / kSlice;
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-  grid_wait();  // the route kernel's results
-  const long long total = (long long)ws_off[batch] * Hkv;
+  // Slices of the sequences before each, per KV head: formed here up to kQThreads
+  // sequences, so that only block lists (where there are any) are waited for.
+  const int32_t* off = ws_off;
+  if (batch <= kQThreads) {
+    int nb;
+    const int v = t < batch ? pair_slices(seqlens[t], B, kk, max_blocks * B, &nb) : 0;
+    int in = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, in, o);
+      if (lane >= o) in += y;
+    }
+    if (lane == 31) s_list[warp] = in;
+    __syncthreads();
+    int base = 0;
+#pragma unroll
+    for (int w = 0; w < kQW; ++w) base += w < warp ? s_list[w] : 0;
+    if (t < batch) s_off[t + 1] = base + in;
+    if (t == 0) s_off[0] = 0;
+    __syncthreads();
+    off = s_off;
+    if (lists) grid_wait();
+  } else {
+    grid_wait();
+  }
+  const long long total = (long long)off[batch] * Hkv;
   // no more blocks than leave each some slices
   const long long most = (total + min_slices - 1) / min_slices;
   const long long grid = most < gridDim.x ? most : gridDim.x;
-  if (blockIdx.x >= grid) return;  // also when there is nothing at all
+  if (blockIdx.x >= grid) {  // also when there is nothing at all
+    grid_wait();  // this kernel's end is to mean that the route kernel has ended too
+    return;
+  }
   const long long s0 = blockIdx.x * total / grid, s1 = (blockIdx.x + 1) * total / grid;
   const int ns = (int)(s1 - s0);
   // the warp's run
@@ -403,7 +433,7 @@ __global__ void __launch_bounds__(kQThreads, 1) q8_split_kernel(
   if (t < kQW * 2) s_pair[t >> 1][t & 1] = -1;
   for (int b0 = 0; b0 < batch; b0 += kQThreads) {
     const int b = b0 + t;
-    if (b < batch && (long long)ws_off[b] * Hkv <= s0 && (long long)ws_off[b + 1] * Hkv > s0)
+    if (b < batch && (long long)off[b] * Hkv <= s0 && (long long)off[b + 1] * Hkv > s0)
       s_b = b;
   }
   __syncthreads();
@@ -418,10 +448,10 @@ __global__ void __launch_bounds__(kQThreads, 1) q8_split_kernel(
     if (i >= w1) return r;
     const long long s = s0 + i;
     int b = b_first;
-    while ((long long)ws_off[b + 1] * Hkv <= s) ++b;
+    while ((long long)off[b + 1] * Hkv <= s) ++b;
     const int L = seqlens[b];
-    const int per = ws_off[b + 1] - ws_off[b];
-    const int in = (int)(s - (long long)ws_off[b] * Hkv);
+    const int per = off[b + 1] - off[b];
+    const int in = (int)(s - (long long)off[b] * Hkv);
     const int g = in / per, k = in - g * per;
     const int e = k / spb, sub = k - e * spb;
     const int last = (L - 1) / B;
@@ -500,10 +530,10 @@ __global__ void __launch_bounds__(kQThreads, 1) q8_split_kernel(
   while (w0 + n < w1) {
     // ---- the pair at the warp's slice n
     const long long pos = s0 + w0 + n;
-    while ((long long)ws_off[b + 1] * Hkv <= pos) ++b;
-    const int per = ws_off[b + 1] - ws_off[b];
-    const int g = (int)((pos - (long long)ws_off[b] * Hkv) / per);
-    const long long pair0 = (long long)ws_off[b] * Hkv + (long long)g * per;
+    while ((long long)off[b + 1] * Hkv <= pos) ++b;
+    const int per = off[b + 1] - off[b];
+    const int g = (int)((pos - (long long)off[b] * Hkv) / per);
+    const long long pair0 = (long long)off[b] * Hkv + (long long)g * per;
     const bool begins = pair0 >= s0 + w0, ends = pair0 + per <= s0 + w1;
     const int stop = ends ? (int)(pair0 + per - s0) - w0 : w1 - w0;
 
@@ -747,9 +777,9 @@ __global__ void __launch_bounds__(kQThreads, 1) q8_split_kernel(
   // first slice of a pair, and its number of slices
   auto pair_first = [&](int p) {
     const int pb = p / Hkv;
-    return (long long)ws_off[pb] * Hkv + (long long)(p - pb * Hkv) * (ws_off[pb + 1] - ws_off[pb]);
+    return (long long)off[pb] * Hkv + (long long)(p - pb * Hkv) * (off[pb + 1] - off[pb]);
   };
-  auto pair_len = [&](int p) { return ws_off[p / Hkv + 1] - ws_off[p / Hkv]; };
+  auto pair_len = [&](int p) { return off[p / Hkv + 1] - off[p / Hkv]; };
   const int E = G * (D / 4);  // float4 of a record
   for (int e = t; e < groups * E; e += kQThreads) {
     const int k = e / E, r = e - k * E;
@@ -792,7 +822,7 @@ __global__ void __launch_bounds__(kQThreads, 1) q8_split_kernel(
   }
   // ---- pairs split between blocks: the last block to arrive joins the records.
   // Only the block's first and last group can be such.
-  __threadfence();
+  grid_wait();  // the counters are 0 (nothing is left to wait for where lists were)
   __syncthreads();
   auto block_of = [&](long long s) { return (int)(((s + 1) * grid + total - 1) / total - 1); };
   if (t < 2) {
@@ -802,74 +832,74 @@ __global__ void __launch_bounds__(kQThreads, 1) q8_split_kernel(
       const long long f = pair_first(p), e = f + pair_len(p);
       if (f < s0 || e > s1) {
         const int parts = block_of(e - 1) - block_of(f) + 1;
+        __threadfence();  // the records, which the barrier has put before this
         if (atomicAdd(&ws_ctr[p], 1) == parts - 1) s_last[t] = p;
+        __threadfence();
       }
     }
   }
   __syncthreads();
-  for (int k = 0; k < 2; ++k) {
-    const int p = s_last[k];
-    if (p < 0) continue;
-    __threadfence();
+  // One pair for the whole block, or one for each half of it
+  const bool two = s_last[0] >= 0 && s_last[1] >= 0;
+  const int half = two && t >= kQThreads / 2 ? 1 : 0;
+  const int p = two ? s_last[half] : max(s_last[0], s_last[1]);
+  if (p < 0) return;
+  {
+    const int nt = two ? kQThreads / 2 : kQThreads, tt = t - half * (kQThreads / 2);
     const long long f = pair_first(p);
     const int xf = block_of(f), parts = block_of(f + pair_len(p) - 1) - xf + 1;
     // the pair is the last of its first block and the first of the others
     auto record = [&](int x) { return ws_part + ((size_t)(xf + x) * 2 + (x == 0 ? 1 : 0)) * rec_g; };
-    // Threads e + E y take the records y, y + PS, ... of the e-th float4; m and l
+    // Threads e + E y take the records y, y + PS, ... of the float4 e, e + PS E, ...; m and l
     // of all records and the threads' sums go through the warps' records' room.
-    float2* ml = reinterpret_cast<float2*>(rec0);                  // [parts][8]
-    float* sums = rec0 + 2 * 8 * kQGridMax;                        // [PS][E][8]
-    const int PS = min(kQThreads / E, kJoinSums / E);
-    const int e = t % E, y = t / E, h = e / (D / 4), d4 = (e - h * (D / 4)) * 4;
-    constexpr int U = 4;
-    float4 pre[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (y < PS && y + u * PS < parts)
-        pre[u] = __ldcg(reinterpret_cast<const float4*>(record(y + u * PS) + h * D + d4));
-    for (int i = t; i < parts * G; i += kQThreads) {
+    float* room = rec0 + half * (kQW * REC / 2);
+    float2* ml = reinterpret_cast<float2*>(room);                  // [parts][8]
+    float* sums = room + 2 * 8 * kQGridMax;                        // [PS - 1][E][8]
+    const int PS = max(1, min(nt / E, 1 + kJoinSums / E));
+    const int y = tt / E;
+    for (int i = tt; i < parts * G; i += nt) {
       const float* r = record(i / G) + G * D + i % G;
       ml[i / G * 8 + i % G] = make_float2(__ldcg(r), __ldcg(r + 8));
     }
     __syncthreads();
-    float num[4] = {0.f, 0.f, 0.f, 0.f}, den = 0.f;
-    if (y < PS) {
-      float M = -INFINITY;
+    for (int e0 = 0; e0 < E; e0 += PS == 1 ? nt : E) {
+      const int e = PS == 1 ? e0 + tt : tt - y * E;
+      const bool in = PS == 1 ? e < E : y < PS;
+      const int h = e / (D / 4), d4 = (e - h * (D / 4)) * 4;
+      float num[4] = {0.f, 0.f, 0.f, 0.f}, den = 0.f;
+      if (in) {
+        float M = -INFINITY;
 #pragma unroll 8
-      for (int x = 0; x < parts; ++x) M = fmaxf(M, ml[x * 8 + h].x);
-      auto add = [&](int x, const float4& o) {
-        const float2 w = ml[x * 8 + h];
-        const float a = w.x == -INFINITY ? 0.f : ex2(w.x - M);
-        num[0] = fmaf(a, o.x, num[0]);
-        num[1] = fmaf(a, o.y, num[1]);
-        num[2] = fmaf(a, o.z, num[2]);
-        num[3] = fmaf(a, o.w, num[3]);
-        den = fmaf(a, w.y, den);
-      };
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (y + u * PS < parts) add(y + u * PS, pre[u]);
+        for (int x = 0; x < parts; ++x) M = fmaxf(M, ml[x * 8 + h].x);
 #pragma unroll 4
-      for (int x = y + U * PS; x < parts; x += PS)
-        add(x, __ldcg(reinterpret_cast<const float4*>(record(x) + h * D + d4)));
-      if (y > 0) {
-        float* sm = sums + ((y - 1) * E + e) * 8;
-        *reinterpret_cast<float4*>(sm) = make_float4(num[0], num[1], num[2], num[3]);
-        sm[4] = den;
+        for (int x = PS == 1 ? 0 : y; x < parts; x += PS) {
+          const float4 o = __ldcg(reinterpret_cast<const float4*>(record(x) + h * D + d4));
+          const float2 w = ml[x * 8 + h];
+          const float a = w.x == -INFINITY ? 0.f : ex2(w.x - M);
+          num[0] = fmaf(a, o.x, num[0]);
+          num[1] = fmaf(a, o.y, num[1]);
+          num[2] = fmaf(a, o.z, num[2]);
+          num[3] = fmaf(a, o.w, num[3]);
+          den = fmaf(a, w.y, den);
+        }
+        if (PS > 1 && y > 0) {
+          float* sm = sums + ((y - 1) * E + e) * 8;
+          *reinterpret_cast<float4*>(sm) = make_float4(num[0], num[1], num[2], num[3]);
+          sm[4] = den;
+        }
       }
-    }
-    __syncthreads();
-    if (y == 0) {
-      for (int z = 1; z < PS; ++z) {
-        const float* sm = sums + ((z - 1) * E + e) * 8;
+      __syncthreads();
+      if (in && (PS == 1 || y == 0)) {
+        for (int z = 1; z < PS; ++z) {
+          const float* sm = sums + ((z - 1) * E + e) * 8;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) num[i] += sm[i];
-        den += sm[4];
+          for (int i = 0; i < 4; ++i) num[i] += sm[i];
+          den += sm[4];
+        }
+        store4(O + ((int64_t)(p / Hkv) * Hq + (p % Hkv) * G + h) * D + d4,
+               make_float4(num[0], num[1], num[2], num[3]), den == 0.f ? 0.f : 1.f / den);
       }
-      store4(O + ((int64_t)(p / Hkv) * Hq + (p % Hkv) * G + h) * D + d4,
-             make_float4(num[0], num[1], num[2], num[3]), den == 0.f ? 0.f : 1.f / den);
     }
-    __syncthreads();
   }
 }
 
@@ -881,8 +911,8 @@ Q8Plan plan_q8(int batch, int Hq, int Hkv, int d, int topk, int max_blocks) {
   auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
   // lists are kept for rows that leave blocks out; with topk >= the candidates of
   // the longest row there are none
-  const size_t lists = topk >= max_blocks - 2 ? 0 : pairs * p.width * sizeof(int32_t);
-  p.off_off = up(lists);
+  p.lists = topk < max_blocks - 2;
+  p.off_off = up(p.lists ? pairs * p.width * sizeof(int32_t) : 0);
   p.off_ctr = up(p.off_off + ((size_t)batch + 1) * sizeof(int32_t));
   p.off_part = up(p.off_ctr + pairs * sizeof(int));
   p.bytes = up(p.off_part + (size_t)kQGridMax * 2 * ((size_t)(Hq / Hkv) * d + 16) * sizeof(float));
@@ -947,7 +977,8 @@ static cudaError_t launch_q8_t(const Q8Plan& p, const void* q, const void* Kp, c
   cfg.dynamicSmemBytes = smem2;
   return cudaLaunchKernelEx(&cfg, q8_split_kernel<T, D, F>, (const T*)q, (const uint8_t*)Kp, Ks,
                             (const uint8_t*)Vp, Vs, table, seqlens, batch, Hq, Hkv, B, max_blocks,
-                            num_pages, p.kk, p.width, kQW, (const int32_t*)ws_idx,
+                            num_pages, p.kk, p.width, p.lists ? 1 : 0, kQW,
+                            (const int32_t*)ws_idx,
                             (const int32_t*)ws_off, ws_part, ws_ctr, (T*)O,
                             scale * 1.4426950408889634f);
 }

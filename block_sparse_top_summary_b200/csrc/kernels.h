@@ -132,6 +132,7 @@ cudaError_t launch_append_q8(void* Kp, float* Ks, void* Vp, float* Vs, ssa_qform
 struct Q8Plan {
   int kk;     // effective top-k: min(topk, max_blocks)
   int width;  // idx row width: kk + 2
+  bool lists;  // whether a row can leave blocks out
   // scratch: block lists (from 0), slices before each sequence, arrivals, partial records
   size_t off_off, off_ctr, off_part, bytes;
 };
