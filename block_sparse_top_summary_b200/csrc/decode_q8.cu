@@ -183,24 +183,30 @@ __device__ __forceinline__ int rank_of(const uint32_t* keys, int n, uint32_t key
   return r;
 }
 
-// block_select_topk with few passes over the scores, for k <= 256.  Each of the
-// 256 threads takes the largest of its candidates; the k-th largest of these, T, is not
-// above the k-th largest score, so whatever is selected is >= T.  The candidates
-// >= T, in index order, are few (about k plus the doubles), and each counts those
-// before it.  A list longer than kListCap (many equal scores) is left to
-// block_select_topk.  2046 candidates, k = 32: 2 us against 6.
+// block_select_topk with few passes over the scores, for k <= 128.  The candidates
+// are dealt to 32, 64 or 128 >= k groups; T, the least of the groups' largest scores, is
+// not above the k-th largest score, so whatever is selected is >= T.  The
+// candidates >= T, in index order, are few (about 110 of 1000 or 2000 for k <= 32),
+// and each counts those before it.  A list longer than kListCap (many equal scores)
+// is left to block_select_topk.  MEASURED.
 // keys: 256 + kListCap words, list: kListCap entries of shared memory.
 __device__ int block_select_quick(const float* sc, int n, int k, int first, int32_t* out,
                                   uint32_t* keys, uint16_t* list, uint32_t* hist, int* sbuf) {
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-  if (k <= 0 || k > 256 || k >= n) return block_select_topk(sc, n, k, first, out, hist, sbuf);
+  if (k <= 0 || k > 128 || k >= n) return block_select_topk(sc, n, k, first, out, hist, sbuf);
   uint32_t best = 0;
   for (int e = t; e < n; e += 256) best = max(best, order_key(sc[e]));
   keys[t] = best;
   __syncthreads();
-  if (rank_of(keys, 256, best, t) == k - 1) sbuf[8] = (int)best;
-  __syncthreads();
-  const uint32_t T = (uint32_t)sbuf[8];
+  // group l: the threads l, l + groups, ...; every warp forms the minimum for itself
+  const int groups = k <= 32 ? 32 : k <= 64 ? 64 : 128;
+  uint32_t T = 0xffffffffu;
+  for (int l = lane; l < groups; l += 32) {
+    uint32_t m = 0;
+    for (int u = l; u < 256; u += groups) m = max(m, keys[u]);
+    T = min(T, m);
+  }
+  T = __reduce_min_sync(0xffffffffu, T);
   // a warp lists a contiguous run
   const int seg = ((n + 255) / 256) * 32, e0 = warp * seg, e1 = min(e0 + seg, n);
   int c = 0;
@@ -250,7 +256,7 @@ __device__ int block_select_quick(const float* sc, int n, int k, int first, int3
 // candidates into the first block's shared memory, which then selects.  The last
 // cluster sums the slices of the batch.
 template <typename T, int D>
-__global__ void __launch_bounds__(256, 2) q8_route_kernel(
+__global__ void __launch_bounds__(256, 4) q8_route_kernel(
     const T* __restrict__ q, const float* __restrict__ S, const int32_t* __restrict__ seqlens,
     int batch, int Hq, int Hkv, int Lmax, int B, int nsum, int kk, int width, int CS,
     int32_t* __restrict__ ws_idx, int* __restrict__ ws_ctr, int32_t* __restrict__ ws_off,
@@ -310,11 +316,11 @@ __global__ void __launch_bounds__(256, 2) q8_route_kernel(
   for (int e = 0; e < SL; ++e) qs[e] = qb[lane * SL + e];
   cluster_wait();
   const float* Sg = S + ((int64_t)b * Hkv + g) * nsum * D + lane * SL;
-  // steps of 32 candidates, dealt to the warps of all blocks
-  for (int j0 = 1 + (rank * 8 + warp) * 32; j0 <= n; j0 += 32 * 8 * CS) {
-    float v[32];
+  // steps of 16 candidates, dealt to the warps of all blocks
+  for (int j0 = 1 + (rank * 8 + warp) * 16; j0 <= n; j0 += 16 * 8 * CS) {
+    float v[16];
 #pragma unroll
-    for (int c = 0; c < 32; ++c) {
+    for (int c = 0; c < 16; ++c) {
       const int j = min(j0 + c, n);
       float x[SL], a = 0.f;
       if constexpr (SL == 4) {
@@ -328,8 +334,19 @@ __global__ void __launch_bounds__(256, 2) q8_route_kernel(
       for (int e = 0; e < SL; ++e) a = fmaf(x[e], qs[e], a);
       v[c] = a;
     }
-    const float dot = reduce32_transpose(v);
-    if (j0 + lane <= n) st_first(sc + j0 + lane - 1, dot * inv_sqrt_d);
+    // lane l and l ^ 16 end with the sum of candidate l % 16
+#pragma unroll
+    for (int half = 8; half >= 1; half >>= 1) {
+      const bool upper = (lane & half) != 0;
+#pragma unroll
+      for (int k = 0; k < half; ++k) {
+        const float send = upper ? v[k] : v[k + half];
+        const float keep = upper ? v[k + half] : v[k];
+        v[k] = keep + __shfl_xor_sync(0xffffffffu, send, half);
+      }
+    }
+    const float dot = v[0] + __shfl_xor_sync(0xffffffffu, v[0], 16);
+    if (lane < 16 && j0 + lane <= n) st_first(sc + j0 + lane - 1, dot * inv_sqrt_d);
   }
   cluster_arrive();
   cluster_wait();
