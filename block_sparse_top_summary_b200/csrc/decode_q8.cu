@@ -39,6 +39,7 @@ namespace {
 constexpr int kQW = 12;                 // warps of the split kernel
 constexpr int kQThreads = 32 * kQW;
 constexpr int kSlice = 16;              // keys a slice
+constexpr int kWholeSlices = 96;        // longest pair that a block takes whole (8 slices a warp)
 constexpr int kQGridMax = 160;          // most blocks of the split grid (148 SMs, one each)
 // Slices in flight or in use a warp: 144 KB (d = 128) or 192 KB (d = 64) a block.
 __host__ __device__ constexpr int q8_stages(int d) { return d == 128 ? 3 : 8; }
@@ -188,7 +189,8 @@ __device__ __forceinline__ int rank_of(const uint32_t* keys, int n, uint32_t key
 // not above the k-th largest score, so whatever is selected is >= T.  The
 // candidates >= T, in index order, are few (about 110 of 1000 or 2000 for k <= 32),
 // and each counts those before it.  A list longer than kListCap (many equal scores)
-// is left to block_select_topk.  MEASURED.
+// is left to block_select_topk.  2046 candidates, k = 32: 2.8 us (4.4 us with the
+// k-th of 256 groups' maxima, found by ranking them, for T).
 // keys: 256 + kListCap words, list: kListCap entries of shared memory.
 __device__ int block_select_quick(const float* sc, int n, int k, int first, int32_t* out,
                                   uint32_t* keys, uint16_t* list, uint32_t* hist, int* sbuf) {
@@ -373,8 +375,8 @@ __global__ void __launch_bounds__(kQThreads, 1) q8_split_kernel(
     const T* __restrict__ q, const uint8_t* __restrict__ Kp, const float* __restrict__ Ks,
     const uint8_t* __restrict__ Vp, const float* __restrict__ Vs,
     const int32_t* __restrict__ table, const int32_t* __restrict__ seqlens, int batch, int Hq,
-    int Hkv, int B, int max_blocks, int num_pages, int kk, int width, int lists, int min_slices,
-    const int32_t* __restrict__ ws_idx, const int32_t* __restrict__ ws_off,
+    int Hkv, int B, int max_blocks, int num_pages, int kk, int width, int lists, int whole_pairs,
+    int min_slices, int32_t* __restrict__ idx_out, const int32_t* __restrict__ ws_idx, const int32_t* __restrict__ ws_off,
     float* __restrict__ ws_part, int* __restrict__ ws_ctr, T* __restrict__ O, float scale_log2) {
   constexpr int TILE = kSlice * D;       // bytes of K (or V) of a slice
   constexpr int KS = D / 16;             // k steps of S
@@ -425,7 +427,7 @@ __global__ void __launch_bounds__(kQThreads, 1) q8_split_kernel(
     if (t == 0) s_off[0] = 0;
     __syncthreads();
     off = s_off;
-    if (lists) grid_wait();
+    if (lists) grid_wait();  // (nothing to wait for where whole_pairs)
   } else {
     grid_wait();
   }
@@ -433,11 +435,28 @@ __global__ void __launch_bounds__(kQThreads, 1) q8_split_kernel(
   // no more blocks than leave each some slices
   const long long most = (total + min_slices - 1) / min_slices;
   const long long grid = most < gridDim.x ? most : gridDim.x;
-  if (blockIdx.x >= grid) {  // also when there is nothing at all
-    grid_wait();  // this kernel's end is to mean that the route kernel has ended too
-    return;
+  long long s0, s1;
+  if (whole_pairs) {
+    // one pair a block, with what the route kernel does for rows read whole
+    const int pb = blockIdx.x / Hkv, per = off[pb + 1] - off[pb];
+    s0 = (long long)off[pb] * Hkv + (long long)(blockIdx.x - pb * Hkv) * per;
+    s1 = s0 + per;
+    const int L = per > 0 ? seqlens[pb] : 0, c = (L + B - 1) / B;
+    if (idx_out != nullptr)
+      for (int i = t; i < width; i += kQThreads)
+        idx_out[(int64_t)blockIdx.x * width + i] = i < c ? i : -1;
+    if (per == 0) {
+      for (int e = t; e < G * D; e += kQThreads) store_out(O + (int64_t)blockIdx.x * G * D + e, 0.f);
+      return;
+    }
+  } else {
+    if (blockIdx.x >= grid) {  // also when there is nothing at all
+      grid_wait();  // this kernel's end is to mean that the route kernel has ended too
+      return;
+    }
+    s0 = blockIdx.x * total / grid;
+    s1 = (blockIdx.x + 1) * total / grid;
   }
-  const long long s0 = blockIdx.x * total / grid, s1 = (blockIdx.x + 1) * total / grid;
   const int ns = (int)(s1 - s0);
   // the warp's run
   const int w0 = (int)((long long)warp * ns / kQW), w1 = (int)((long long)(warp + 1) * ns / kQW);
@@ -839,6 +858,7 @@ __global__ void __launch_bounds__(kQThreads, 1) q8_split_kernel(
   }
   // ---- pairs split between blocks: the last block to arrive joins the records.
   // Only the block's first and last group can be such.
+  if (whole_pairs) return;
   grid_wait();  // the counters are 0 (nothing is left to wait for where lists were)
   __syncthreads();
   auto block_of = [&](long long s) { return (int)(((s + 1) * grid + total - 1) / total - 1); };
@@ -953,8 +973,37 @@ static cudaError_t launch_q8_t(const Q8Plan& p, const void* q, const void* Kp, c
   if (e != cudaSuccess) return e;
   e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
+  constexpr int stages = q8_stages(D);
+  const size_t smem2 = (size_t)kQW * 8 * (D + 2) * sizeof(float) +
+                       (size_t)kQW * 8 * sizeof(float4) +
+                       (size_t)kQW * stages * 2 * kSlice * D;
+  e = cudaFuncSetAttribute(q8_split_kernel<T, D, F>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           (int)smem2);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr{};
+  cudaLaunchConfig_t cfg{};
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  auto split = [&](unsigned grid, bool whole) {
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kQThreads);
+    cfg.dynamicSmemBytes = smem2;
+    return cudaLaunchKernelEx(&cfg, q8_split_kernel<T, D, F>, (const T*)q, (const uint8_t*)Kp, Ks,
+                              (const uint8_t*)Vp, Vs, table, seqlens, batch, Hq, Hkv, B,
+                              max_blocks, num_pages, p.kk, p.width, p.lists ? 1 : 0,
+                              whole ? 1 : 0, kQW, idx_out, (const int32_t*)ws_idx,
+                              (const int32_t*)ws_off, ws_part, ws_ctr, (T*)O,
+                              scale * 1.4426950408889634f);
+  };
+  // Few short rows read whole need neither lists nor a split: one launch, a pair a
+  // block.  Two launches and one, us: 1 row of 100 tokens (8 / 2 heads) 10.3, 8.2; of 777
+  // (4 / 1) 14.3, 12.3; 16 rows of 1500 (32 / 8) 21.5, 16.4; but 1 row of 3000 (8 pairs)
+  // 16.4, 22.5 and 64 rows of 1500 (512 pairs) 46.6, 59.4.
+  if (!p.lists && batch * (long long)Hkv <= sms && max_blocks * (B / kSlice) <= kWholeSlices)
+    return split((unsigned)(batch * Hkv), true);
+
   // Few pairs of long rows: several blocks score a pair's summaries, as many as
-  // the GPU takes at once (2 an SM) and as leave each warp a step of 32.
+  // the GPU takes at once (2 an SM) and as leave each warp two steps of 16.
   int CS = 1;
   while (CS < 8 && batch * (long long)Hkv * CS * 2 <= 2 * sms && max_blocks >= CS * 2 * 256) CS *= 2;
   const size_t smem1 = sizeof(float) * (D + 512 + kListCap + kListCap / 2 + (size_t)max_blocks);
@@ -963,41 +1012,21 @@ static cudaError_t launch_q8_t(const Q8Plan& p, const void* q, const void* Kp, c
                              (int)smem1);
     if (e != cudaSuccess) return e;
   }
-  cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeClusterDimension;
   attr.val.clusterDim.x = CS;
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(batch * Hkv + 1) * CS);
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = smem1;
-  cfg.stream = st;
-  cfg.attrs = &attr;
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, q8_route_kernel<T, D>, (const T*)q, S, seqlens, batch, Hq, Hkv,
                          max_blocks * B, B, max_blocks, p.kk, p.width, CS, ws_idx, ws_ctr, ws_off,
                          (T*)O, idx_out, 1.0f / sqrtf((float)D));
   if (e != cudaSuccess) return e;
-  constexpr int stages = q8_stages(D);
-  const size_t smem2 = (size_t)kQW * 8 * (D + 2) * sizeof(float) +
-                       (size_t)kQW * 8 * sizeof(float4) +
-                       (size_t)kQW * stages * 2 * kSlice * D;
-  const int grid = sms < kQGridMax ? sms : kQGridMax;
-  e = cudaFuncSetAttribute(q8_split_kernel<T, D, F>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           (int)smem2);
-  if (e != cudaSuccess) return e;
   attr = cudaLaunchAttribute{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3(kQThreads);
-  cfg.dynamicSmemBytes = smem2;
-  return cudaLaunchKernelEx(&cfg, q8_split_kernel<T, D, F>, (const T*)q, (const uint8_t*)Kp, Ks,
-                            (const uint8_t*)Vp, Vs, table, seqlens, batch, Hq, Hkv, B, max_blocks,
-                            num_pages, p.kk, p.width, p.lists ? 1 : 0, kQW,
-                            (const int32_t*)ws_idx,
-                            (const int32_t*)ws_off, ws_part, ws_ctr, (T*)O,
-                            scale * 1.4426950408889634f);
+  return split((unsigned)(sms < kQGridMax ? sms : kQGridMax), false);
 }
 
 cudaError_t launch_decode_q8(const Q8Plan& p, const void* q, const void* Kp, const float* Ks,

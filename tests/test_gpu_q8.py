@@ -478,6 +478,82 @@ def test_decode_selection_of_long_rows(ssa, topk, ties):
     _check_decode(cache, q, L, B, topk, got, idx, "f32")
 
 
+def test_decode_selection_at_the_largest_cache(ssa):
+    # 16384 blocks, the most that a cache may have
+    B, d, L = 16, 64, [16 * 16384 - 3, 16 * 9000]
+    cache = list(_cache("e4m3", d, B, 1, L, seed=24))
+    q = torch.randn(2, 8, d, generator=torch.Generator().manual_seed(25))
+    for topk in (32, 100):
+        got, idx = _run_decode(ssa, cache, q, L, B, topk)
+        _check_decode(cache, q, L, B, topk, got, idx, "f32")
+
+
+@pytest.mark.parametrize("topk", [1, 1 << 30])
+def test_decode_more_rows_than_threads(ssa, topk):
+    # over 384 rows the slices' sums come from the route kernel; some rows are empty
+    B, d, n = 16, 64, 700
+    r = np.random.default_rng(26)
+    L = r.integers(0, 90, n)
+    cache = _cache("i8", d, B, 1, L.tolist(), seed=26)
+    q = torch.randn(n, 2, d, generator=torch.Generator().manual_seed(27)).bfloat16()
+    got, idx = _run_decode(ssa, cache, q, L, B, topk)
+    _check_decode(cache, q, L, B, topk, got, idx, "bf16")
+
+
+def test_pools_past_4_gb(ssa):
+    # the last pages of pools of 5.2 GB: byte offsets past 32 bits
+    B, d, Hkv, pages = 128, 128, 8, 40000
+    K = torch.empty(pages, Hkv, B, d, dtype=torch.int8, device=DEV)
+    V = torch.empty_like(K)
+    Ks, Vs = (torch.zeros(pages, Hkv, device=DEV) for _ in range(2))
+    L = np.array([300, 129])
+    table = np.array([[pages - 1, 35000, pages - 3], [34000, pages - 2, -1]])
+    cu = np.array([0, 300, 429])
+    slots = np.concatenate([table[b, np.arange(n) // B] * B + np.arange(n) % B
+                            for b, n in enumerate(L)])
+    g = torch.Generator().manual_seed(28)
+    k, v = (torch.randn(429, Hkv, d, generator=g) for _ in range(2))
+    S = torch.zeros(2, Hkv, 3, d, device=DEV)
+    ssa.ssa_append_paged_q8(K, Ks, V, Vs, S, _dev(slots), _dev(cu), _dev(L), k.to(DEV), v.to(DEV),
+                            B)
+    q = torch.randn(2, 16, d, generator=g)
+    used = table[table >= 0]
+    small = np.full_like(table, -1)
+    small[table >= 0] = np.arange(5)
+    at = torch.from_numpy(used).to(DEV)
+    cache = [x[at].cpu() for x in (K, Ks, V, Vs)] + [S.cpu(), small]
+    zero = torch.zeros(5, Hkv, B, d, dtype=torch.int8)
+    one = torch.zeros(5, Hkv)
+    ref = O.append_paged_q8(_np(zero), _np(one), _np(zero), _np(one), None,
+                            np.concatenate([small[b, np.arange(n) // B] * B + np.arange(n) % B
+                                            for b, n in enumerate(L)]), cu, L, _np(k), _np(v), B,
+                            "i8")
+    for b in range(2):  # rows behind a sequence are never written: compare the others
+        for p in range(L[b]):
+            i, row = small[b, p // B], p % B
+            assert np.array_equal(_np(cache[0][i, :, row]), ref[0][i, :, row])
+    assert np.array_equal(_np(cache[1]), ref[1]) and np.array_equal(_np(cache[3]), ref[3])
+    out, idx = ssa.ssa_decode_paged_q8(q.to(DEV), K, Ks, V, Vs, S, _dev(table), _dev(L), B, 1)
+    torch.cuda.synchronize()
+    for x in (cache[0], cache[2]):  # not written, and not to matter
+        x[2, :, 300 - 256:] = 0
+        x[4, :, 1:] = 0
+    _check_decode(cache, q, L, B, 1, out, idx, "f32")
+
+
+def test_decode_nan_query_stays_in_its_head(ssa):
+    B, d, L = 16, 64, [200, 90]
+    cache = _cache("e4m3", d, B, 2, L, seed=31)
+    q = torch.randn(2, 8, d, generator=torch.Generator().manual_seed(31))
+    clean, _ = _run_decode(ssa, cache, q, L, B, 1 << 20)
+    q[0, 1, 3], q[1, 6, 0] = float("nan"), float("inf")
+    got, _ = _run_decode(ssa, cache, q, L, B, 1 << 20)
+    bad = torch.zeros(2, 8, dtype=torch.bool)
+    bad[0, 1] = bad[1, 6] = True
+    assert torch.isnan(got.cpu()[bad]).all()
+    assert torch.equal(got.cpu()[~bad], clean.cpu()[~bad])
+
+
 def test_decode_scale_argument_loud_caches_and_quiet_queries(ssa):
     # scales far from 1 on both sides: codes and f16 parts must not leave their range
     B, d, L = 32, 64, [200, 77]
@@ -586,6 +662,65 @@ def test_decode_on_another_stream_in_a_graph_and_twice_at_once(ssa):
 
 
 # ------------------------------------------------------------------- together
+def test_plan_and_append_in_a_graph_and_on_another_stream(ssa):
+    # one captured step (plan of more than 8192 slots, append, decode), replayed
+    # with other lengths and tokens in the same buffers, against eager calls
+    B, d, Hkv, n, mb, cap = 16, 64, 2, 6, 300, 9000
+    r = np.random.default_rng(40)
+    pages = n * mb + 5
+    order = r.permutation(pages)
+
+    def fresh():
+        return dict(K=torch.zeros(pages, Hkv, B, d, dtype=torch.int8, device=DEV),
+                    V=torch.zeros(pages, Hkv, B, d, dtype=torch.int8, device=DEV),
+                    Ks=torch.zeros(pages, Hkv, device=DEV), Vs=torch.zeros(pages, Hkv, device=DEV),
+                    S=torch.zeros(n, Hkv, mb, d, device=DEV),
+                    have=torch.zeros(n, dtype=torch.int32, device=DEV),
+                    want=torch.zeros(n, dtype=torch.int32, device=DEV),
+                    table=torch.full((n, mb), -1, dtype=torch.int32, device=DEV),
+                    ring=_dev(order), pool=_dev(np.array([0, pages])),
+                    k=torch.zeros(cap, Hkv, d, device=DEV, dtype=torch.bfloat16),
+                    v=torch.zeros(cap, Hkv, d, device=DEV, dtype=torch.bfloat16),
+                    q=torch.zeros(n, 4, d, device=DEV, dtype=torch.bfloat16))
+
+    def step(s, stream=None):
+        _, cu, slots, _ = ssa.ssa_page_plan(s["have"], s["want"], s["table"], s["ring"], s["pool"],
+                                            B, cap, got=s["have"], pool_out=s["pool"],
+                                            stream=stream)
+        ssa.ssa_append_paged_q8(s["K"], s["Ks"], s["V"], s["Vs"], s["S"], slots, cu, s["have"],
+                                s["k"], s["v"], B, stream=stream)
+        return ssa.ssa_decode_paged_q8(s["q"], s["K"], s["Ks"], s["V"], s["Vs"], s["S"],
+                                       s["table"], s["have"], B, 4, stream=stream)
+
+    wants = [[3000, 17, 0, 900, 1, 4700], [3001, 18, 1500, 0, 2, 4701], [2990, 18, 1501, 700, 3, 0]]
+    eager, captured, other = fresh(), fresh(), fresh()
+    graph = torch.cuda.CUDAGraph()
+    warm = torch.cuda.Stream()
+    with torch.cuda.stream(warm):
+        step(fresh())
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        out = step(captured)
+    side = torch.cuda.Stream()
+    for i, want in enumerate(wants):
+        g = torch.Generator().manual_seed(41 + i)
+        new = {x: torch.randn(eager[x].shape, generator=g).to(DEV, torch.bfloat16) for x in "kvq"}
+        for s in (eager, captured, other):
+            for x in "kvq":
+                s[x].copy_(new[x])
+            s["want"].copy_(_dev(np.array(want)))
+        ref = step(eager)
+        graph.replay()
+        side.wait_stream(torch.cuda.current_stream())
+        got = step(other, stream=side)
+        torch.cuda.synchronize()
+        assert eager["have"].tolist() == want
+        for s, o in ((captured, out), (other, got)):
+            for x in eager:
+                assert torch.equal(eager[x], s[x]), x
+            assert torch.equal(ref[0], o[0]) and torch.equal(ref[1], o[1])
+
+
 @pytest.mark.parametrize("fmt,dtype", [("e4m3", "bf16"), ("i8", "f32")])
 def test_serving_steps_plan_append_decode(ssa, fmt, dtype):
     """Prompts, decode steps, a rollback, a finished and a refused request, as a
