@@ -101,6 +101,25 @@ __device__ __forceinline__ void mma16(float (&c)[4], uint32_t a0, uint32_t a1, u
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// One m16n8k32 tile on int8 operands: c += A . B, exact.
+__device__ __forceinline__ void mma32(int (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                      uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// |x| < 64 as d0 + 2^-7 d1 + 2^-14 d2, whole numbers up to 64: exact for a bf16 x from
+// 2^-7 up, and off by at most 2^-15 below.
+__device__ __forceinline__ void digits3(float x, uint32_t (&d)[3]) {
+  const float a = rintf(x), y = (x - a) * 128.f, b = rintf(y), c = rintf((y - b) * 128.f);
+  d[0] = (uint32_t)(int)a & 255u;
+  d[1] = (uint32_t)(int)b & 255u;
+  d[2] = (uint32_t)(int)c & 255u;
+}
+
 // c = A . B (no accumulator to clear).
 __device__ __forceinline__ void mma16_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                             uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -394,7 +413,14 @@ __global__ void __launch_bounds__(kQThreads, 1) q8_split_kernel(
                                 ? (kQW * REC / 2 - 2 * 8 * kQGridMax) / 8
                                 : 0;
   static_assert(kQW * REC >= 2 * 2 * 8 * kQGridMax, "m and l of two pairs' records");
-  // q in fp32 keeps a low part; bf16 is exact in f16
+  // q against e4m3 codes, or in fp32: f16 against keys turned into f16, with a low part
+  // in fp32.  q in bf16 against int8 codes: three int8 digits against the codes
+  // themselves, which saves turning K (410 -> 350 instructions a slice; under a
+  // sustained load, where the clock falls, 32 ragged rows 131 -> 123 us).  e4m3 has
+  // no such tile: the one that PTX offers here turns its operands into f16 as well
+  // (9 to 12 cycles an SM quarter for k = 32 at a latency of 47, f16 8.3 for k = 16 at 24),
+  // and was slower (56 -> 65 us for 128K keys).
+  constexpr bool kDigits = sizeof(T) == 2 && F == SSA_I8;
   constexpr bool kLow = sizeof(T) == 4;
   extern __shared__ __align__(128) unsigned char q8_smem[];
   __shared__ int s_b, s_groups;
@@ -573,13 +599,16 @@ __global__ void __launch_bounds__(kQThreads, 1) q8_split_kernel(
     const bool begins = pair0 >= s0 + w0, ends = pair0 + per <= s0 + w1;
     const int stop = ends ? (int)(pair0 + per - s0) - w0 : w1 - w0;
 
-    // Fragments of q.  Lane (gr, tq) holds coordinates 64 c + 16 tq + 4 s + i of
-    // head gr: k step 4 c + s, words b0 (i < 2) and b1; a power of two brings
-    // the head's largest coordinate into [2^14, 2^15).
-    uint32_t qa[KS][2], ql[kLow ? KS : 1][2];
-    float qscale[2];  // of heads 2 tq and 2 tq + 1
+    // Fragments of q: lane (gr, tq) holds coordinates 64 c + 16 tq + i of head gr.  A
+    // power of two brings the head's largest coordinate into [2^kTop, 2^(kTop + 1)).
+    // Digits: k step 2 c + p of 32 has i = 8 p ..; f16: k step 4 c + s
+    // of 16 has i = 4 s ..
+    uint32_t qa[kDigits ? 3 * (D / 32) : KS][2], ql[kLow ? KS : 1][2];
+    float qscale[2];  // of heads 2 tq and 2 tq + 1; NaN for one with a NaN or infinity
     {
-      float v[D / 64][16], m = 0.f;
+      constexpr int kTop = kDigits ? 5 : 14;
+      float v[D / 64][16];
+      uint32_t m = 0;
       const T* qp = q + ((int64_t)b * Hq + g * G + (gr < G ? gr : 0)) * D + 16 * tq;
 #pragma unroll
       for (int c = 0; c < D / 64; ++c) {
@@ -588,25 +617,43 @@ __global__ void __launch_bounds__(kQThreads, 1) q8_split_kernel(
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
           v[c][e] = gr < G ? v[c][e] : 0.f;
-          m = fmaxf(m, fabsf(v[c][e]));
+          m = max(m, __float_as_uint(v[c][e]) & 0x7fffffffu);
         }
       }
-      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-      const int ex = max((int)(__float_as_uint(m) >> 23) - 127 - 14, -126);
+      m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+      m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+      const int ex = max((int)(m >> 23) - 127 - kTop, -126);
       const float up = __uint_as_float((uint32_t)(127 - ex) << 23);
-      const float back = __uint_as_float((uint32_t)(127 + ex) << 23) * scale_log2;
+      const float back = m >= 0x7f800000u
+                             ? __uint_as_float(0x7fc00000u)
+                             : __uint_as_float((uint32_t)(127 + ex) << 23) * scale_log2;
       qscale[0] = __shfl_sync(0xffffffffu, back, 8 * tq);
       qscale[1] = __shfl_sync(0xffffffffu, back, 8 * tq + 4);
+      if constexpr (!kDigits) {
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        const float* x = v[ks >> 2] + 4 * (ks & 3);
-        if constexpr (kLow) {
-          split_half2(x[0] * up, x[1] * up, qa[ks][0], ql[ks][0]);
-          split_half2(x[2] * up, x[3] * up, qa[ks][1], ql[ks][1]);
-        } else {
-          qa[ks][0] = half2_bits(x[0] * up, x[1] * up);
-          qa[ks][1] = half2_bits(x[2] * up, x[3] * up);
+        for (int ks = 0; ks < KS; ++ks) {
+          const float* x = v[ks >> 2] + 4 * (ks & 3);
+          if constexpr (kLow) {
+            split_half2(x[0] * up, x[1] * up, qa[ks][0], ql[ks][0]);
+            split_half2(x[2] * up, x[3] * up, qa[ks][1], ql[ks][1]);
+          } else {
+            qa[ks][0] = half2_bits(x[0] * up, x[1] * up);
+            qa[ks][1] = half2_bits(x[2] * up, x[3] * up);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int w = 0; w < D / 16; ++w) {  // word w & 1 of k step w >> 1
+          uint32_t word[3] = {0, 0, 0};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint32_t dg[3];
+            digits3(v[w >> 2][4 * (w & 3) + e] * up, dg);
+#pragma unroll
+            for (int i = 0; i < 3; ++i) word[i] |= dg[i] << (8 * e);
+          }
+#pragma unroll
+          for (int i = 0; i < 3; ++i) qa[i * (D / 32) + (w >> 1)][w & 1] = word[i];
         }
       }
     }
@@ -624,23 +671,46 @@ __global__ void __launch_bounds__(kQThreads, 1) q8_split_kernel(
       const int rows = __float_as_int(mi.x);
       const uint32_t so = (uint32_t)st * (2 * TILE);
       if (rows > 0) {
-        // S^T = K q^T of 16 keys, even and odd k steps apart
-        float se[4], sd[4];
+        // S^T = K q^T of 16 keys
+        float sv[4];
+        if constexpr (!kDigits) {
+          float se[4], sd[4];  // even and odd k steps
 #pragma unroll
-        for (int c = 0; c < D / 64; ++c) {
-          const uint4 u = lds16((c == 0 ? k_at : k_at2) + so);
-          const uint4 v = lds16((c == 0 ? k_at : k_at2) + so + 8 * D);
+          for (int c = 0; c < D / 64; ++c) {
+            const uint4 u = lds16((c == 0 ? k_at : k_at2) + so);
+            const uint4 v = lds16((c == 0 ? k_at : k_at2) + so + 8 * D);
 #pragma unroll
-          for (int s = 0; s < 4; ++s) {
-            uint32_t a0, a1, a2, a3;
-            q8_to_half4<F>(s == 0 ? u.x : s == 1 ? u.y : s == 2 ? u.z : u.w, a0, a2);
-            q8_to_half4<F>(s == 0 ? v.x : s == 1 ? v.y : s == 2 ? v.z : v.w, a1, a3);
-            const int ks = 4 * c + s;
-            if (ks == 0) mma16_first(se, a0, a1, a2, a3, qa[ks][0], qa[ks][1]);
-            else if (ks == 1) mma16_first(sd, a0, a1, a2, a3, qa[ks][0], qa[ks][1]);
-            else mma16(s & 1 ? sd : se, a0, a1, a2, a3, qa[ks][0], qa[ks][1]);
-            if constexpr (kLow) mma16(s & 1 ? sd : se, a0, a1, a2, a3, ql[ks][0], ql[ks][1]);
+            for (int s = 0; s < 4; ++s) {
+              uint32_t a0, a1, a2, a3;
+              q8_to_half4<F>(s == 0 ? u.x : s == 1 ? u.y : s == 2 ? u.z : u.w, a0, a2);
+              q8_to_half4<F>(s == 0 ? v.x : s == 1 ? v.y : s == 2 ? v.z : v.w, a1, a3);
+              const int ks = 4 * c + s;
+              if (ks == 0) mma16_first(se, a0, a1, a2, a3, qa[ks][0], qa[ks][1]);
+              else if (ks == 1) mma16_first(sd, a0, a1, a2, a3, qa[ks][0], qa[ks][1]);
+              else mma16(s & 1 ? sd : se, a0, a1, a2, a3, qa[ks][0], qa[ks][1]);
+              if constexpr (kLow) mma16(s & 1 ? sd : se, a0, a1, a2, a3, ql[ks][0], ql[ks][1]);
+            }
           }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sv[e] = se[e] + sd[e];
+        } else {
+          int sg[3][4] = {};  // by digit
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c) {
+            const uint4 u = lds16((c == 0 ? k_at : k_at2) + so);
+            const uint4 v = lds16((c == 0 ? k_at : k_at2) + so + 8 * D);
+#pragma unroll
+            for (int i = 0; i < 3; ++i) {
+              const uint32_t(*w)[2] = qa + i * (D / 32) + 2 * c;
+              mma32(sg[i], u.x, v.x, u.y, v.y, w[0][0], w[0][1]);
+              mma32(sg[i], u.z, v.z, u.w, v.w, w[1][0], w[1][1]);
+            }
+          }
+          // |sums of d0| <= 2^20, so 2^7 times that and the sums of d1 fit 32 bits
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            sv[e] = fmaf((float)(sg[0][e] * 128 + sg[1][e]), 1.f / 128.f,
+                         (float)sg[2][e] * (1.f / 16384.f));
         }
         uint32_t r[4][D / 32];  // V rows va, vb, va + 8, vb + 8: columns gr D / 8 ...
 #pragma unroll
@@ -659,7 +729,7 @@ __global__ void __launch_bounds__(kQThreads, 1) q8_split_kernel(
 #pragma unroll
         for (int y = 0; y < 2; ++y)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) x[y][e] = (se[2 * y + e] + sd[2 * y + e]) * (mi.y * qscale[e]);
+          for (int e = 0; e < 2; ++e) x[y][e] = sv[2 * y + e] * (mi.y * qscale[e]);
         if (rows < kSlice) {
 #pragma unroll
           for (int y = 0; y < 2; ++y)
@@ -892,7 +962,8 @@ __global__ void __launch_bounds__(kQThreads, 1) q8_split_kernel(
     float* room = rec0 + half * (kQW * REC / 2);
     float2* ml = reinterpret_cast<float2*>(room);                  // [parts][8]
     float* sums = room + 2 * 8 * kQGridMax;                        // [PS - 1][E][8]
-    const int PS = max(1, min(nt / E, 1 + kJoinSums / E));
+    // (PS, and so the order of the sums, does not depend on which pairs meet here)
+    const int PS = max(1, min(kQThreads / 2 / E, 1 + kJoinSums / E));
     const int y = tt / E;
     for (int i = tt; i < parts * G; i += nt) {
       const float* r = record(i / G) + G * D + i % G;

@@ -661,6 +661,25 @@ def test_decode_on_another_stream_in_a_graph_and_twice_at_once(ssa):
         assert torch.equal(outs[1][0], whole[i][0])
 
 
+@pytest.mark.parametrize("G,d,topk", [(4, 128, 1 << 20), (1, 64, 1 << 20), (8, 128, 5)])
+def test_decode_repeats_bitwise(ssa, G, d, topk):
+    # rows split between blocks: the block that joins a row's parts changes from run
+    # to run, the order of the sums must not
+    B, L = 32, [5000, 33, 2500, 700, 4100]
+    cache = _cache("e4m3", d, B, 2, L, seed=33)
+    K, Ks, V, Vs, S = (x.to(DEV) for x in cache[:5])
+    table, lens = _dev(cache[5]), _dev(np.asarray(L))
+    q = torch.randn(5, 2 * G, d, generator=torch.Generator().manual_seed(33)).to(DEV)
+    for t in (torch.bfloat16, torch.float32):
+        ref = None
+        for i in range(200):
+            out, _ = ssa.ssa_decode_paged_q8(q.to(t), K, Ks, V, Vs, S, table, lens, B, topk)
+            if i % 7 == 0:  # another load on the GPU beside some of them
+                torch.empty(1 << 22, device=DEV).fill_(i)
+            ref = out if ref is None else ref
+            assert torch.equal(out, ref)
+
+
 # ------------------------------------------------------------------- together
 def test_plan_and_append_in_a_graph_and_on_another_stream(ssa):
     # one captured step (plan of more than 8192 slots, append, decode), replayed
