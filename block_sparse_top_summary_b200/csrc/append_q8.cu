@@ -10,10 +10,13 @@
 //
 // A block of threads takes a unit, K or V, and a group of heads.  It is as large as
 // a tile of B rows with kChunks 8-element chunks a thread (bf16: 8, fp32: 4), and
-// loads the next head's rows before it works on the present one's.  Units of few
-// rows (decode steps) are left to single warps, a head each, without a barrier.
-// 52233 tokens of 8 heads, d = 128, B = 64 (bf16): 229 us with one block of 256
-// threads a tile and a bisection of dependent loads, MEASURED us this way.
+// has the next two heads' rows under way while it works on the present one's.  Units
+// of few rows (decode steps) are left to single warps, a head each, without a barrier.
+// 52233 tokens of 8 heads, d = 128, B = 64 (bf16 to e4m3; 0.32 GB): 229 us with one block of
+// 256 threads a tile and a bisection of dependent loads, 64 us (5.0 TB/s) this way, with
+// the arithmetic at 60% of the issue slots: 8 chunks a thread (4: 69 us) and
+// mixed-precision FMAs on the bf16 elements (unpacked first: 76 us) cut that.  64 single
+// tokens: 17 us before, 4.4 us.
 //
 // Units of sequence b start at floor(cu[b] / B) + 2 b: n new tokens touch at most
 // floor(n / B) + 2 blocks, so the ranges do not meet, and a unit's sequence is found
@@ -109,7 +112,6 @@ __global__ void __launch_bounds__(512) append_q8_kernel(
   constexpr int RPW = 32 / CPR;     // rows a warp step
   constexpr int kChunks = sizeof(T) == 2 ? 8 : 4;
   __shared__ uint32_t s_max[2][16];
-  __shared__ __align__(16) float s_sum[16 * RPW][D];
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5, warps = blockDim.x >> 5;
   const bool is_v = blockIdx.y & 1;
   const int g0 = (blockIdx.y >> 1) * heads, g1 = min(g0 + heads, Hkv);
@@ -253,17 +255,44 @@ __global__ void __launch_bounds__(512) append_q8_kernel(
     }
     return;
   }
-  // the block a head
+  // the block a head, the next ones on their way to shared memory: a thread copies its
+  // own chunks and reads them back, so its own waits are enough
   const int rps = warps * RPW, rr = t / CPR, cc = t % CPR;
-  Raw8<T> raw[kChunks], next[kChunks];
-  load(g0, rr, cc, rps, raw);
-  float old = r0 > 0 ? Ps[g0] : 0.f, old_next = 0.f;
-  for (int g = g0; g < g1; ++g) {
-    if (g + 1 < g1) {
-      load(g + 1, rr, cc, rps, next);
-      if (r0 > 0) old_next = Ps[g + 1];
+  constexpr int stages = 2;  // 3 and 4 were no faster
+  constexpr int PIECES = kChunks * (int)sizeof(T) / 2;  // 16-byte pieces a thread and head
+  extern __shared__ __align__(16) uint4 ring[];         // [stages][PIECES][threads]
+  float* s_sum = reinterpret_cast<float*>(ring + stages * PIECES * blockDim.x);  // [rps][D]
+  auto fetch = [&](int g, int stage) {
+    if (g < g1) {
+      const T* p = x + (int64_t)g * head_stride + (int64_t)rr * tok_stride + cc * 8;
+      const int64_t step = rps * tok_stride;
+      uint32_t to = (uint32_t)__cvta_generic_to_shared(ring + (stage * PIECES) * blockDim.x + t);
+#pragma unroll
+      for (int i = 0; i < kChunks; ++i, p += step)
+#pragma unroll
+        for (int k = 0; k < PIECES / kChunks; ++k, to += blockDim.x * 16)
+          if (rr + i * rps < nr)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to),
+                         "l"(reinterpret_cast<const uint4*>(p) + k)
+                         : "memory");
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  for (int i = 0; i < stages; ++i) fetch(g0 + i, i);
+  float old = r0 > 0 ? Ps[g0] : 0.f, old_next = 0.f;
+  int stage = 0;
+  for (int g = g0; g < g1; ++g) {
+    if (r0 > 0 && g + 1 < g1) old_next = Ps[g + 1];
+    asm volatile("cp.async.wait_group %0;" ::"n"(stages - 1) : "memory");
+    Raw8<T> raw[kChunks];
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i)
+#pragma unroll
+      for (int k = 0; k < PIECES / kChunks; ++k)
+        raw[i].v[k] = ring[(stage * PIECES + i * (PIECES / kChunks) + k) * blockDim.x + t];
     uint32_t m = largest(rr, rps, raw);
+    fetch(g + stages, stage);
+    stage = stage == stages - 1 ? 0 : stage + 1;
     uint32_t* sm = s_max[(g - g0) & 1];  // the other one may still be read
     if (lane == 0) sm[warp] = m;
     __syncthreads();
@@ -272,20 +301,18 @@ __global__ void __launch_bounds__(512) append_q8_kernel(
     const float scale = write(g, rr, cc, rps, raw, m, old, sum);
     if (t == 0) Ps[g] = scale;  // the old one was read before the barrier
     if (mean) {
-      *reinterpret_cast<float4*>(&s_sum[rr][cc * 8]) = make_float4(sum[0], sum[1], sum[2], sum[3]);
-      *reinterpret_cast<float4*>(&s_sum[rr][cc * 8 + 4]) =
-          make_float4(sum[4], sum[5], sum[6], sum[7]);
+      float4* mine = reinterpret_cast<float4*>(s_sum + rr * D + cc * 8);
+      mine[0] = make_float4(sum[0], sum[1], sum[2], sum[3]);
+      mine[1] = make_float4(sum[4], sum[5], sum[6], sum[7]);
       __syncthreads();
       for (int c = t; c < D; c += blockDim.x) {
         float a = 0.f;
 #pragma unroll 8
-        for (int w = 0; w < rps; ++w) a += s_sum[w][c];
+        for (int w = 0; w < rps; ++w) a += s_sum[w * D + c];
         Sj[(int64_t)g * max_blocks * D + c] = a * (scale / (float)B);
       }
       // s_sum is written again only behind the next head's barrier
     }
-#pragma unroll
-    for (int i = 0; i < kChunks; ++i) raw[i] = next[i];
     old = old_next;
   }
 }
@@ -300,12 +327,19 @@ static cudaError_t launch_append_q8_t(void* Kp, float* Ks, void* Vp, float* Vs, 
   const int chunks = sizeof(T) == 2 ? 8 : 4;
   const int threads = (B * (D / 8) / chunks + 31) / 32 * 32;  // 32 .. 512
   const long long units = T_max / B + 2LL * batch;
-  // All heads of a unit in one block where the units alone fill the GPU (148 SMs, a
-  // few blocks each), else fewer.
+  // All heads of a unit in one block where the units alone fill the GPU (2 blocks for
+  // each of 148 SMs), else fewer.
   int heads = Hkv;
-  while (heads > 1 && units * 2 * ((Hkv + heads - 1) / heads) < 4 * 148) heads = (heads + 1) / 2;
+  while (heads > 1 && units * 2 * ((Hkv + heads - 1) / heads) < 2 * 148) heads = (heads + 1) / 2;
   const dim3 grid((unsigned)units, (unsigned)(2 * ((Hkv + heads - 1) / heads)));
-  append_q8_kernel<T, D, F><<<grid, threads, 0, st>>>(
+  // two heads' rows (16 KB each for 64 rows of 128 in bf16), and the threads' sums
+  const int smem = threads * (2 * chunks * 8 * (int)sizeof(T) + 8 * (int)sizeof(float));
+  if (smem > 47 * 1024) {  // the static array counts too
+    const cudaError_t e = cudaFuncSetAttribute(
+        append_q8_kernel<T, D, F>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+  }
+  append_q8_kernel<T, D, F><<<grid, threads, smem, st>>>(
       (uint8_t*)Kp, Ks, (uint8_t*)Vp, Vs, S, slots, cu, seqlens, (const T*)kn, (const T*)vn,
       tok_stride, head_stride, batch, T_max, Hkv, heads, B, max_blocks, num_pages);
   return cudaGetLastError();
