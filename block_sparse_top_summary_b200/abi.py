@@ -504,24 +504,27 @@ def ssa_sparse_attn_bwd(Q, K, V, O, dO, lse, idx, cnt, B: int, scale: float | No
 
 # ------------------------------------------------- page plan and 8-bit paged cache
 # A serving step makes these calls back to back and their kernels take a few
-# microseconds, so the checks are one expression a tensor, and the current
-# device and stream are read without building torch's Python objects for them.
+# microseconds, so the checks are one expression a call (spelt out by _refuse where it
+# fails), and the current device and stream are read without building torch's
+# Python objects for them.
 _device = torch._C._cuda_getDevice
 _current_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _arg(n: str, t: torch.Tensor, dtype: torch.dtype, shape: tuple, dev: int) -> int:
-    """The address of an argument that has this type and shape, is contiguous and
-    on the current device (the one the library launches on)."""
-    if (t.dtype is not dtype or t.shape != shape or t.get_device() != dev
-            or not t.is_contiguous()):
+def _refuse(dev: int, *args):
+    """Raises for the first of ``(name, tensor, dtype, shape)`` that does not have this
+    type and shape, is not contiguous or not on the current device (the one the
+    library launches on).  For calls whose own quick test of the same has failed."""
+    for n, t, dtype, shape in args:
+        if t is None:
+            continue
         _need(t, n)
         if t.dtype is not dtype:
             raise TypeError(f"{n} must be {dtype}, not {t.dtype}")
         if t.shape != shape:
             raise ValueError(f"{n} must have shape {list(shape)}, not {list(t.shape)}")
-        raise ValueError(f"{n} is on cuda:{t.get_device()}, the current device is cuda:{dev}")
-    return t.data_ptr()
+        if t.get_device() != dev:
+            raise ValueError(f"{n} is on cuda:{t.get_device()}, the current device is cuda:{dev}")
 
 
 def _launch_on(stream, dev: int, own=()):
@@ -550,7 +553,23 @@ def ssa_page_plan(have, want, page_table, ring, pool, B: int, max_new: int, keep
     i32, dev = torch.int32, _device()
     batch, max_blocks = page_table.shape
     num_pages = ring.numel()
-    rows, at, own = (batch,), have.device, []
+    rows, two, own = (batch,), (2,), []
+    if (have.dtype is not i32 or have.shape != rows or want.dtype is not i32
+            or want.shape != rows or page_table.dtype is not i32 or ring.dtype is not i32
+            or ring.dim() != 1 or pool.dtype is not i32 or pool.shape != two
+            or not (have.get_device() == want.get_device() == page_table.get_device()
+                    == ring.get_device() == pool.get_device() == dev)
+            or not (have.is_contiguous() and want.is_contiguous() and page_table.is_contiguous()
+                    and ring.is_contiguous() and pool.is_contiguous())):
+        _refuse(dev, ("have", have, i32, rows), ("want", want, i32, rows),
+                ("page_table", page_table, i32, (batch, max_blocks)),
+                ("ring", ring, i32, (num_pages,)), ("pool", pool, i32, two))
+    if keep is not None:
+        _refuse(dev, ("keep", keep, i32, rows))
+    if got is not None or cu is not None or slots is not None or pool_out is not None:
+        _refuse(dev, ("got", got, i32, rows), ("cu", cu, i32, (batch + 1,)),
+                ("slots", slots, i32, (max_new,)), ("pool_out", pool_out, i32, two))
+    at = have.device
     if got is None:
         own.append(got := torch.empty(batch, dtype=i32, device=at))
     if cu is None:
@@ -559,16 +578,9 @@ def ssa_page_plan(have, want, page_table, ring, pool, B: int, max_new: int, keep
         own.append(slots := torch.empty(max_new, dtype=i32, device=at))
     if pool_out is None:
         own.append(pool_out := torch.empty(2, dtype=i32, device=at))
-    if len(own) < 4:
-        _arg("got", got, i32, rows, dev)
-        _arg("cu", cu, i32, (batch + 1,), dev)
-        _arg("slots", slots, i32, (max_new,), dev)
-        _arg("pool_out", pool_out, i32, (2,), dev)
     status = load_library().ssa_page_plan(
-        _arg("have", have, i32, rows, dev), _arg("want", want, i32, rows, dev),
-        None if keep is None else _arg("keep", keep, i32, rows, dev), batch, B,
-        _arg("page_table", page_table, i32, (batch, max_blocks), dev), max_blocks, num_pages,
-        _arg("ring", ring, i32, (num_pages,), dev), _arg("pool", pool, i32, (2,), dev),
+        have.data_ptr(), want.data_ptr(), None if keep is None else keep.data_ptr(), batch, B,
+        page_table.data_ptr(), max_blocks, num_pages, ring.data_ptr(), pool.data_ptr(),
         pool_out.data_ptr(), got.data_ptr(), cu.data_ptr(), slots.data_ptr(), max_new,
         _launch_on(stream, dev, own))
     _check("ssa_page_plan", status)
@@ -578,21 +590,25 @@ def ssa_page_plan(have, want, page_table, ring, pool, B: int, max_new: int, keep
 _Q8_FORMATS = {torch.float8_e4m3fn: SSA_E4M3, torch.int8: SSA_I8}
 
 
-def _q8_format(Kp: torch.Tensor) -> int:
-    fmt = _Q8_FORMATS.get(Kp.dtype)
+def _q8_cache(Kp, Ks, Vp, Vs, S, B: int, dev: int, batch: int, max_blocks: int):
+    """Checks the cache; returns its format, pages, heads and head dimension."""
+    code, f32 = Kp.dtype, torch.float32
+    fmt = _Q8_FORMATS.get(code)
     if fmt is None:
-        raise TypeError(f"unsupported cache dtype {Kp.dtype} (float8_e4m3fn or int8)")
-    return fmt
-
-
-def _q8_cache(Kp, Ks, Vp, Vs, B: int, dev: int):
-    """The format, sizes and addresses of the cache tensors."""
-    fmt = _q8_format(Kp)
+        raise TypeError(f"unsupported cache dtype {code} (float8_e4m3fn or int8)")
     num_pages, Hkv, _, d = Kp.shape
     pool, scales = (num_pages, Hkv, B, d), (num_pages, Hkv)
-    return (fmt, num_pages, Hkv, d, _arg("Kp", Kp, Kp.dtype, pool, dev),
-            _arg("Ks", Ks, torch.float32, scales, dev), _arg("Vp", Vp, Kp.dtype, pool, dev),
-            _arg("Vs", Vs, torch.float32, scales, dev))
+    if (Kp.shape != pool or Vp.shape != pool or Vp.dtype is not code or Ks.shape != scales
+            or Vs.shape != scales or Ks.dtype is not f32 or Vs.dtype is not f32
+            or not (Kp.get_device() == Vp.get_device() == Ks.get_device() == Vs.get_device() == dev)
+            or not (Kp.is_contiguous() and Vp.is_contiguous() and Ks.is_contiguous()
+                    and Vs.is_contiguous())):
+        _refuse(dev, ("Kp", Kp, code, pool), ("Ks", Ks, f32, scales), ("Vp", Vp, code, pool),
+                ("Vs", Vs, f32, scales))
+    if S is not None and (S.dtype is not f32 or S.shape != (batch, Hkv, max_blocks, d)
+                          or S.get_device() != dev or not S.is_contiguous()):
+        _refuse(dev, ("S", S, f32, (batch, Hkv, max_blocks, d)))
+    return fmt, num_pages, Hkv, d
 
 
 def ssa_append_paged_q8(Kp, Ks, Vp, Vs, S, slots, cu, seqlens, k_new, v_new, B: int,
@@ -609,11 +625,17 @@ def ssa_append_paged_q8(Kp, Ks, Vp, Vs, S, slots, cu, seqlens, k_new, v_new, B: 
     """
     i32, dev = torch.int32, _device()
     batch, T = seqlens.shape[0], slots.numel()
-    fmt, num_pages, Hkv, d, kp, ks, vp, vs = _q8_cache(Kp, Ks, Vp, Vs, B, dev)
     if S is not None:
         max_blocks = S.shape[2]
     elif max_blocks is None:
         raise ValueError("max_blocks is needed when there are no summaries")
+    fmt, num_pages, Hkv, d = _q8_cache(Kp, Ks, Vp, Vs, S, B, dev, batch, max_blocks)
+    if (slots.dtype is not i32 or slots.dim() != 1 or cu.dtype is not i32
+            or cu.shape != (batch + 1,) or seqlens.dtype is not i32 or seqlens.dim() != 1
+            or not (slots.get_device() == cu.get_device() == seqlens.get_device() == dev)
+            or not (slots.is_contiguous() and cu.is_contiguous() and seqlens.is_contiguous())):
+        _refuse(dev, ("slots", slots, i32, (T,)), ("cu", cu, i32, (batch + 1,)),
+                ("seqlens", seqlens, i32, (batch,)))
     strides, new = k_new.stride(), (T, Hkv, d)
     if (k_new.shape != new or v_new.shape != new or k_new.dtype is not v_new.dtype
             or k_new.get_device() != dev or v_new.get_device() != dev
@@ -621,12 +643,10 @@ def ssa_append_paged_q8(Kp, Ks, Vp, Vs, S, slots, cu, seqlens, k_new, v_new, B: 
         raise ValueError(f"k_new and v_new must be {list(new)} on the current device (cuda:{dev}), "
                          "of one dtype, of equal strides and contiguous in d")
     status = load_library().ssa_append_paged_q8(
-        kp, ks, vp, vs, fmt,
-        None if S is None else _arg("S", S, torch.float32, (batch, Hkv, max_blocks, d), dev),
-        _arg("slots", slots, i32, (T,), dev), _arg("cu", cu, i32, (batch + 1,), dev),
-        _arg("seqlens", seqlens, i32, (batch,), dev), k_new.data_ptr(), v_new.data_ptr(),
-        _dtype_code(k_new), strides[0], strides[1], batch, T, Hkv, d, B, max_blocks, num_pages,
-        _launch_on(stream, dev))
+        Kp.data_ptr(), Ks.data_ptr(), Vp.data_ptr(), Vs.data_ptr(), fmt,
+        None if S is None else S.data_ptr(), slots.data_ptr(), cu.data_ptr(), seqlens.data_ptr(),
+        k_new.data_ptr(), v_new.data_ptr(), _dtype_code(k_new), strides[0], strides[1], batch, T,
+        Hkv, d, B, max_blocks, num_pages, _launch_on(stream, dev))
     _check("ssa_append_paged_q8", status)
     return Kp, Ks, Vp, Vs, S
 
@@ -651,19 +671,25 @@ def ssa_decode_paged_q8(q, Kp, Ks, Vp, Vs, S, page_table, seqlens, B: int, topk:
     all of its cache; ``S`` may be None when ``topk >= max_blocks - 2``.
     ``workspace``: ``ssa_decode_paged_q8_workspace_size`` bytes, uint8.
     """
-    i32, dev = torch.int32, _device()
-    fmt, num_pages, Hkv, d, kp, ks, vp, vs = _q8_cache(Kp, Ks, Vp, Vs, B, dev)
-    heads = q.shape
+    i32, dev, heads = torch.int32, _device(), q.shape
     batch, Hq, _ = heads
     max_blocks = page_table.shape[1]
+    fmt, num_pages, Hkv, d = _q8_cache(Kp, Ks, Vp, Vs, S, B, dev, batch, max_blocks)
     width = (topk if topk < max_blocks else max_blocks) + 2
-    qp, own = _arg("q", q, q.dtype, (batch, Hq, d), dev), []
+    if (heads[2] != d or page_table.dtype is not i32 or page_table.shape != (batch, max_blocks)
+            or seqlens.dtype is not i32 or seqlens.shape != (batch,)
+            or not (q.get_device() == page_table.get_device() == seqlens.get_device() == dev)
+            or not (q.is_contiguous() and page_table.is_contiguous() and seqlens.is_contiguous())):
+        _refuse(dev, ("q", q, q.dtype, (batch, Hq, d)),
+                ("page_table", page_table, i32, (batch, max_blocks)),
+                ("seqlens", seqlens, i32, (batch,)))
+    own = []
     if O is None:
         own.append(O := torch.empty_like(q))
     else:
-        _arg("O", O, q.dtype, heads, dev)
+        _refuse(dev, ("O", O, q.dtype, heads))
     if idx is not None:
-        _arg("idx", idx, i32, (batch, Hkv, width), dev)
+        _refuse(dev, ("idx", idx, i32, (batch, Hkv, width)))
     elif want_idx:
         own.append(idx := torch.empty(batch, Hkv, width, dtype=i32, device=q.device))
     if workspace is None:
@@ -671,15 +697,13 @@ def ssa_decode_paged_q8(q, Kp, Ks, Vp, Vs, S, page_table, seqlens, B: int, topk:
             ssa_decode_paged_q8_workspace_size(batch, Hq, Hkv, d, B, topk, max_blocks),
             dtype=torch.uint8, device=q.device))
     else:
-        _arg("workspace", workspace, torch.uint8, (workspace.numel(),), dev)
+        _refuse(dev, ("workspace", workspace, torch.uint8, (workspace.numel(),)))
     status = load_library().ssa_decode_paged_q8(
-        qp, _dtype_code(q), kp, ks, vp, vs, fmt,
-        None if S is None else _arg("S", S, torch.float32, (batch, Hkv, max_blocks, d), dev),
-        _arg("page_table", page_table, i32, (batch, max_blocks), dev), max_blocks, num_pages,
-        _arg("seqlens", seqlens, i32, (batch,), dev), batch, Hq, Hkv, d, B, topk,
-        d ** -0.5 if scale is None else scale, O.data_ptr(),
-        None if idx is None else idx.data_ptr(), workspace.data_ptr(), workspace.numel(),
-        _launch_on(stream, dev, own))
+        q.data_ptr(), _dtype_code(q), Kp.data_ptr(), Ks.data_ptr(), Vp.data_ptr(), Vs.data_ptr(),
+        fmt, None if S is None else S.data_ptr(), page_table.data_ptr(), max_blocks, num_pages,
+        seqlens.data_ptr(), batch, Hq, Hkv, d, B, topk, d ** -0.5 if scale is None else scale,
+        O.data_ptr(), None if idx is None else idx.data_ptr(), workspace.data_ptr(),
+        workspace.numel(), _launch_on(stream, dev, own))
     _check("ssa_decode_paged_q8", status)
     return O, idx
 

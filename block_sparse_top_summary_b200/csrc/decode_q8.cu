@@ -3,30 +3,38 @@
 // With k = Ks[page, g] * code, the scale of a block is a factor of its logits, and
 // the scale of V a factor of the block's share of the output:
 //   x_t = (scale ks) (q . kcode_t),   O = sum_blocks vs (sum_t p_t vcode_t) / l,
-// so the codes go to the tensor cores as they are: both formats are exact in f16.
-// HBM-bound; two launches:
-//   1. route (one block per sequence and KV head, and one that sums the slices of
-//      the batch): scores the summaries of rows that have more candidates than
-//      are kept and writes their block lists; rows that keep every block are not
-//      scored and need no list.
+// so the codes go to the tensor cores unscaled: both formats are exact in f16, and
+// int8 has tiles of its own.  HBM-bound; two launches, or one for few short rows:
+//   1. route: a cluster of 1 to 8 blocks a sequence and KV head (a pair) scores the
+//      summaries of rows that have more candidates than are kept, and selects; rows
+//      that keep every block are not scored and need no list.
 //   2. split attention.  The work is cut into slices of 16 keys; block x of the
 //      grid takes an equal contiguous run of all slices, whatever the sequences'
-//      lengths, and its warps take the run's slices in turn.  Each warp copies its
-//      own slices into its own ring of shared memory (cp.async, 16 bytes a
-//      thread), so nothing is waited for across warps but at the end of a
-//      sequence and head, where the warps' states (m, l, O) are joined.  A
-//      sequence and head that is split between blocks is finished by the last of
-//      them, from the blocks' partial records in order.
+//      lengths, and each of its 12 warps an equal contiguous run of those.  A warp
+//      copies its own slices into its own ring of shared memory (cp.async, 16
+//      bytes a thread; 96 KB of a block's are under way) and keeps its own m, l and O,
+//      so nothing is waited for across warps until the block's run is done.  A pair that
+//      lies within a warp's run is written at once; the others' records are joined
+//      in shared memory, and a pair that is split between blocks is finished by the
+//      last of them, from the blocks' records in order.  The kernel starts while the
+//      route kernel runs (programmatic dependent launch) and waits only for lists.
+// Measured (B200, CUDA graph): 128K keys of 8 heads, d = 128, e4m3, read whole (0.27 GB):
+// 56 us, of which the stream takes 41 (6.5 TB/s), start, join and the last blocks' part
+// the rest; 32 ragged rows of up to 16K keys, int8 (0.67 GB): 115 us; 64 rows of 65536 keys,
+// top-32 (0.27 GB of summaries, 0.28 GB of codes): 110 us.  A first form with a barrier
+// of all warps at every pair's end, the heads as the tiles' rows and a serial join took 74,
+// 175 and 138 us.
 //
 // Fragments.  m16n8k16 tiles, f16 in and fp32 out, with the cache as the row operand:
 // S^T = K q^T has a tile's 16 rows for the slice's keys and its 8 columns for the
-// group's heads, O^T = V^T P^T its rows for 16 coordinates.  So no row is idle, and
-// the f16 pairs of a code word are its operands as they come.  q (fp32) and P are
-// held as the sum of two f16, 22 bits: two products with one row operand and one
-// accumulator.  A thread reads 16 bytes of a key row at a time: the order of the
-// coordinates within a product is free, as long as q has the same.  The order of
-// the keys is pi(row), chosen with the chunk swizzle so that neither K nor V
-// reads have bank conflicts.  P^T is the S^T tile transposed (movmatrix).
+// group's heads, O^T = V^T P^T its rows for 16 coordinates.  So no row is idle (with
+// the heads as rows half of them are), and the f16 pairs of a code word are its
+// operands as they come.  q in fp32 and P are held as the sum of two f16, 22 bits:
+// two products with one row operand and one accumulator.  A thread reads 16 bytes
+// of a key row at a time: the order of the coordinates within a product is free, as
+// long as q has the same.  The order of the keys is pi(row), chosen with the chunk
+// swizzle so that neither K nor V reads have bank conflicts.  P^T is the S^T tile
+// transposed (movmatrix).
 #include "common.cuh"
 #include "kernels.h"
 #include "q8.cuh"
@@ -338,7 +346,7 @@ __global__ void __launch_bounds__(256, 4) q8_route_kernel(
   cluster_wait();
   const float* Sg = S + ((int64_t)b * Hkv + g) * nsum * D + lane * SL;
   // steps of 16 candidates, dealt to the warps of all blocks
-  for (int j0 = 1 + (rank * 8 + warp) * 16; j0 <= n; j0 += 16 * 8 * CS) {
+  for (int j0 = 1 + (rank * 8 + warp) * 16; kk > 0 && j0 <= n; j0 += 16 * 8 * CS) {
     float v[16];
 #pragma unroll
     for (int c = 0; c < 16; ++c) {

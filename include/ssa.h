@@ -435,7 +435,8 @@ ssa_status ssa_decode_append_paged(void* Kp, void* Vp, ssa_dtype dtype, float* S
  * token; pool_out = {head, count}; the granted rows' new entries of page_table
  * and the returned pages' entries of ring.  Entries of page_table behind a row's
  * blocks keep what they held; a returned page beyond what the ring can hold
- * (a page that was free already) is dropped.
+ * (a page that was free already) is dropped.  A row that lacks a page it should
+ * hold gets slots of -1 for that block's tokens or for all of its tokens.
  * All int32: have, want, keep, got: [batch]; page_table: [batch, max_blocks];
  * ring: [num_pages]; pool, pool_out: [2]; cu: [batch + 1]; slots: [max_new].
  * got may be have, and pool_out may be pool; nothing else may overlap.
@@ -491,8 +492,11 @@ ssa_status ssa_append_paged_q8(void* Kp, float* Ks, void* Vp, float* Vs, ssa_qfo
 
 /*
  * One decode step over the 8-bit paged cache: ssa_decode_paged with K and V the
- * values that the codes stand for.  q, O: [batch, Hq, d] of `dtype`; sums and
- * softmax in fp32, q and P as sums of two f16 (22 bits) on the tensor cores.
+ * values that the codes stand for.  q, O: [batch, Hq, d] of `dtype`.  Sums and
+ * softmax are in fp32; on the tensor cores P is the sum of two f16 (22 bits), and
+ * so is q in fp32, relative to each head's largest coordinate; q in bf16 is exact
+ * but for coordinates below 2^-12 of that, which are held to 2^-20 of it.  The
+ * unnormalised sums of P times V have to stay within fp32's range.
  *
  * A sequence with at most topk candidate blocks attends its whole cache and its
  * summaries are not read; S may be NULL when topk >= max_blocks - 2, which is

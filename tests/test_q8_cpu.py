@@ -98,13 +98,20 @@ def test_decode_q8_rejections(lib):
     assert abi.ssa_decode_paged_q8_workspace_size(64, 32, 8, 128, 64, 1 << 30, 16384) < 16 << 20
 
 
-def test_binding_checks():
+def test_binding_refuses_what_is_not_on_a_gpu(monkeypatch):
+    monkeypatch.setattr(abi, "_device", lambda: 0)
+    K, s = torch.zeros(4, 2, 16, 64, dtype=torch.int8), torch.zeros(4, 2)
+    i = torch.zeros(1, dtype=torch.int32)
     with pytest.raises(TypeError):
-        abi._q8_format(torch.zeros(1, dtype=torch.uint8))
-    assert abi._q8_format(torch.zeros(1, dtype=torch.int8)) == 1
-    x = torch.zeros(3, 4)
-    with pytest.raises(ValueError, match="CUDA"):
-        abi._arg("x", x, torch.float32, (3, 4), 0)
+        abi._q8_cache(K.view(torch.uint8), s, K, s, None, 16, 0, 1, 4)
+    with pytest.raises(ValueError, match="Kp must be a CUDA tensor"):
+        abi.ssa_decode_paged_q8(torch.zeros(1, 4, 64), K, s, K, s, None, i[None], i, 16, 9)
+    with pytest.raises(ValueError, match="Kp must be a CUDA tensor"):
+        abi.ssa_append_paged_q8(K, s, K, s, None, i, i, i, s, s, 16, max_blocks=1)
+    with pytest.raises(ValueError, match="max_blocks"):
+        abi.ssa_append_paged_q8(K, s, K, s, None, i, i, i, s, s, 16)
+    with pytest.raises(ValueError, match="have must be a CUDA tensor"):
+        abi.ssa_page_plan(i, i, i[None], i, torch.zeros(2, dtype=torch.int32), 16, 4)
 
 
 def test_oracle_codes_match_torch_e4m3_and_closed_forms():
