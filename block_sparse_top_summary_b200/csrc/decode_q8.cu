@@ -47,7 +47,7 @@ namespace {
 constexpr int kQW = 12;                 // warps of the split kernel
 constexpr int kQThreads = 32 * kQW;
 constexpr int kSlice = 16;              // keys a slice
-constexpr int kWholeSlices = 96;        // longest pair that a block takes whole (8 slices a warp)
+constexpr int kWholeSlices = 96;        // most slices of a pair that a block takes whole
 constexpr int kQGridMax = 160;          // most blocks of the split grid (148 SMs, one each)
 // Slices in flight or in use a warp: 144 KB (d = 128) or 192 KB (d = 64) a block.
 __host__ __device__ constexpr int q8_stages(int d) { return d == 128 ? 3 : 8; }
@@ -471,18 +471,20 @@ __global__ void __launch_bounds__(kQThreads, 1) q8_split_kernel(
   const long long grid = most < gridDim.x ? most : gridDim.x;
   long long s0, s1;
   if (whole_pairs) {
-    // one pair a block, with what the route kernel does for rows read whole
+    // one pair a block, with what the route kernel does where there is one
     const int pb = blockIdx.x / Hkv, per = off[pb + 1] - off[pb];
     s0 = (long long)off[pb] * Hkv + (long long)(blockIdx.x - pb * Hkv) * per;
     s1 = s0 + per;
-    const int L = per > 0 ? seqlens[pb] : 0, c = (L + B - 1) / B;
-    if (idx_out != nullptr)
-      for (int i = t; i < width; i += kQThreads)
-        idx_out[(int64_t)blockIdx.x * width + i] = i < c ? i : -1;
-    if (per == 0) {
-      for (int e = t; e < G * D; e += kQThreads) store_out(O + (int64_t)blockIdx.x * G * D + e, 0.f);
-      return;
+    if (!lists) {
+      const int L = per > 0 ? seqlens[pb] : 0, c = (L + B - 1) / B;
+      if (idx_out != nullptr)
+        for (int i = t; i < width; i += kQThreads)
+          idx_out[(int64_t)blockIdx.x * width + i] = i < c ? i : -1;
+      if (per == 0)
+        for (int e = t; e < G * D; e += kQThreads)
+          store_out(O + (int64_t)blockIdx.x * G * D + e, 0.f);
     }
+    if (per == 0) return;
   } else {
     if (blockIdx.x >= grid) {  // also when there is nothing at all
       grid_wait();  // this kernel's end is to mean that the route kernel has ended too
@@ -1074,12 +1076,14 @@ static cudaError_t launch_q8_t(const Q8Plan& p, const void* q, const void* Kp, c
                               (const int32_t*)ws_off, ws_part, ws_ctr, (T*)O,
                               scale * 1.4426950408889634f);
   };
-  // Few short rows read whole need neither lists nor a split: one launch, a pair a
-  // block.  Two launches and one, us: 1 row of 100 tokens (8 / 2 heads) 10.3, 8.2; of 777
-  // (4 / 1) 14.3, 12.3; 16 rows of 1500 (32 / 8) 21.5, 16.4; but 1 row of 3000 (8 pairs)
-  // 16.4, 22.5 and 64 rows of 1500 (512 pairs) 46.6, 59.4.
-  if (!p.lists && batch * (long long)Hkv <= sms && max_blocks * (B / kSlice) <= kWholeSlices)
-    return split((unsigned)(batch * Hkv), true);
+  // Few pairs of few slices go to a block each and need no split: without lists in
+  // one launch.  Split and whole, us: 1 row of 100 tokens (8 / 2 heads) 10.3, 8.2; of 777
+  // (4 / 1) 14.3, 12.3; 16 rows of 1500 (32 / 8) 21.5, 16.4; 24 ragged rows, top-8 blocks of
+  // 128 (8 / 4) 25.6, 22.6; but 1 row of 3000 (8 pairs) 16.4, 22.5 and 64 rows of 1500
+  // (512 pairs) 46.6, 59.4.
+  const int most = max_blocks < p.width ? max_blocks : p.width;  // blocks of a pair
+  const bool whole = batch * (long long)Hkv <= sms && most * (B / kSlice) <= kWholeSlices;
+  if (whole && !p.lists) return split((unsigned)(batch * Hkv), true);
 
   // Few pairs of long rows: several blocks score a pair's summaries, as many as
   // the GPU takes at once (2 an SM) and as leave each warp two steps of 16.
@@ -1105,7 +1109,8 @@ static cudaError_t launch_q8_t(const Q8Plan& p, const void* q, const void* Kp, c
   attr = cudaLaunchAttribute{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
-  return split((unsigned)(sms < kQGridMax ? sms : kQGridMax), false);
+  return whole ? split((unsigned)(batch * Hkv), true)
+               : split((unsigned)(sms < kQGridMax ? sms : kQGridMax), false);
 }
 
 cudaError_t launch_decode_q8(const Q8Plan& p, const void* q, const void* Kp, const float* Ks,
