@@ -423,11 +423,11 @@ __global__ void __launch_bounds__(kQThreads, 1) q8_split_kernel(
   static_assert(kQW * REC >= 2 * 2 * 8 * kQGridMax, "m and l of two pairs' records");
   // q against e4m3 codes, or in fp32: f16 against keys turned into f16, with a low part
   // in fp32.  q in bf16 against int8 codes: three int8 digits against the codes
-  // themselves, which saves turning K (410 -> 350 instructions a slice; under a
-  // sustained load, where the clock falls, 32 ragged rows 131 -> 123 us).  e4m3 has
-  // no such tile: the one that PTX offers here turns its operands into f16 as well
-  // (9 to 12 cycles an SM quarter for k = 32 at a latency of 47, f16 8.3 for k = 16 at 24),
-  // and was slower (56 -> 65 us for 128K keys).
+  // themselves, which saves turning K (410 -> 392 instructions a slice; 32 ragged rows 116 -> 115 us, and under a sustained
+  // load, where int8 meets the power limit, 132 -> 127 us).  e4m3 has no such
+  // tile: the one that PTX offers here turns its operands into f16 as well (9 to 12
+  // cycles an SM quarter for k = 32 at a latency of 47, f16 8.3 for k = 16 at 24), and
+  // was slower (56 -> 65 us for 128K keys).
   constexpr bool kDigits = sizeof(T) == 2 && F == SSA_I8;
   constexpr bool kLow = sizeof(T) == 4;
   extern __shared__ __align__(128) unsigned char q8_smem[];
