@@ -198,12 +198,14 @@ __device__ __forceinline__ void st_first(float* p, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(r), "f"(v) : "memory");
 }
 
-// Entries of keys[0 .. n) (n up to a multiple of 4, the rest 0) that come before key
-// at position i: the larger ones, and the equal ones of a lower position.
-__device__ __forceinline__ int rank_of(const uint32_t* keys, int n, uint32_t key, int i) {
+// Entries of keys[u0], keys[u0 + 1], .. 4 of every `step` below n (n up to a multiple of 4,
+// the rest 0), that come before key at position i: the larger ones, and the equal ones
+// of a lower position.
+__device__ __forceinline__ int rank_of(const uint32_t* keys, int u0, int step, int n, uint32_t key,
+                                       int i) {
   int r = 0;
 #pragma unroll 4
-  for (int u = 0; u < n; u += 4) {
+  for (int u = u0; u < n; u += step) {
     const uint4 k = *reinterpret_cast<const uint4*>(keys + u);
     r += (k.x > key || (k.x == key && u < i)) + (k.y > key || (k.y == key && u + 1 < i)) +
          (k.z > key || (k.z == key && u + 2 < i)) + (k.w > key || (k.w == key && u + 3 < i));
@@ -267,10 +269,14 @@ __device__ int block_select_quick(const float* sc, int n, int k, int first, int3
   }
   if (t < 4 && m + t < kListCap) lk[m + t] = 0;  // up to a multiple of 4
   __syncthreads();
+  // two threads a candidate, each against half of the list
   int done = 0;
-  for (int i0 = 0; i0 < m; i0 += 256) {
-    const int i = i0 + t;
-    const bool take = i < m && rank_of(lk, m, lk[i], i) < k;
+  for (int i0 = 0; i0 < m; i0 += 128) {
+    const int i = i0 + (t >> 1);
+    const uint32_t key = i < m ? lk[i] : 0u;
+    int r = i < m ? rank_of(lk, (t & 1) * 4, 8, m, key, i) : k;
+    r += __shfl_xor_sync(0xffffffffu, r, 1);
+    const bool take = (t & 1) == 0 && r < k;
     int tot;
     const int at = block_excl_scan(take ? 1 : 0, sbuf, &tot);
     if (take) out[done + at] = first + (int)list[i];
@@ -313,6 +319,11 @@ __global__ void __launch_bounds__(256, 4) q8_route_kernel(
   if (t == 0 && rank == 0) ws_ctr[bg] = 0;
   const int b = bg / Hkv, g = bg - (bg / Hkv) * Hkv, G = Hq / Hkv;
   const int L = seqlens[b];
+  float qsum = 0.f;  // (read beside the length)
+  if (kk < nsum - 2 && t < D) {
+#pragma unroll 4
+    for (int h = 0; h < G; ++h) qsum += (float)q[((int64_t)b * Hq + g * G + h) * D + t];
+  }
   const bool valid = L >= 1 && L <= Lmax;
   const int last = valid ? (L - 1) / B : 0;
   const int n = valid ? max(last - 1, 0) : 0;  // candidates 1 .. last - 1
@@ -334,11 +345,7 @@ __global__ void __launch_bounds__(256, 4) q8_route_kernel(
   uint32_t* keys = hist + 256;                                       // [256 + kListCap]
   uint16_t* list = reinterpret_cast<uint16_t*>(keys + 256 + kListCap);  // [kListCap]
   float* sc = reinterpret_cast<float*>(list + kListCap);             // [nsum]
-  if (t < D) {
-    float s = 0.f;
-    for (int h = 0; h < G; ++h) s += (float)q[((int64_t)b * Hq + g * G + h) * D + t];
-    qb[t] = s / (float)G;
-  }
+  if (t < D) qb[t] = qsum / (float)G;
   __syncthreads();
   float qs[SL];
 #pragma unroll
@@ -381,14 +388,14 @@ __global__ void __launch_bounds__(256, 4) q8_route_kernel(
   cluster_wait();
   if (rank > 0) return;
   int32_t* row = ws_idx + (int64_t)bg * width;
-  block_select_quick(sc, n, kk, 1, row + 1, keys, list, hist, sbuf);
-  if (t == 0) {
-    row[0] = 0;
-    row[kk + 1] = last;
-  }
-  if (idx_out != nullptr) {
-    __syncthreads();
-    for (int p = t; p < width; p += 256) idx_out[(int64_t)bg * width + p] = row[p];
+  // the list by way of shared memory where that holds it (hist is free by then)
+  int32_t* out = kk <= 128 ? reinterpret_cast<int32_t*>(hist) : row + 1;
+  block_select_quick(sc, n, kk, 1, out, keys, list, hist, sbuf);
+  __syncthreads();
+  for (int p = t; p < width; p += 256) {
+    const int j = p == 0 ? 0 : p == kk + 1 ? last : out[p - 1];
+    row[p] = j;
+    if (idx_out != nullptr) idx_out[(int64_t)bg * width + p] = j;
   }
 }
 
@@ -461,7 +468,6 @@ __global__ void __launch_bounds__(kQThreads, 1) q8_split_kernel(
     if (t == 0) s_off[0] = 0;
     __syncthreads();
     off = s_off;
-    if (lists) grid_wait();  // (nothing to wait for where whole_pairs)
   } else {
     grid_wait();
   }
@@ -484,10 +490,13 @@ __global__ void __launch_bounds__(kQThreads, 1) q8_split_kernel(
         for (int e = t; e < G * D; e += kQThreads)
           store_out(O + (int64_t)blockIdx.x * G * D + e, 0.f);
     }
-    if (per == 0) return;
+    if (per == 0) {
+      grid_wait();  // this kernel's end is to mean that the route kernel has ended too
+      return;
+    }
   } else {
     if (blockIdx.x >= grid) {  // also when there is nothing at all
-      grid_wait();  // this kernel's end is to mean that the route kernel has ended too
+      grid_wait();
       return;
     }
     s0 = blockIdx.x * total / grid;
@@ -510,6 +519,7 @@ __global__ void __launch_bounds__(kQThreads, 1) q8_split_kernel(
   }
   __syncthreads();
   const int b_first = s_b;
+  if (lists) grid_wait();
 
   // What a slice is: page * Hkv + g (or -1: no keys), first row | rows << 8.
   struct Slice {
