@@ -692,18 +692,21 @@ def ssa_decode_paged_q8(q, Kp, Ks, Vp, Vs, S, page_table, seqlens, B: int, topk:
         _refuse(dev, ("idx", idx, i32, (batch, Hkv, width)))
     elif want_idx:
         own.append(idx := torch.empty(batch, Hkv, width, dtype=i32, device=q.device))
-    if workspace is None:
-        own.append(workspace := torch.empty(
-            ssa_decode_paged_q8_workspace_size(batch, Hq, Hkv, d, B, topk, max_blocks),
-            dtype=torch.uint8, device=q.device))
-    else:
-        _refuse(dev, ("workspace", workspace, torch.uint8, (workspace.numel(),)))
+    at = ws_bytes = 0
+    if workspace is not None:
+        ws_bytes = workspace.numel()
+        _refuse(dev, ("workspace", workspace, torch.uint8, (ws_bytes,)))
+        at = workspace.data_ptr()
+    elif (ws_bytes := ssa_decode_paged_q8_workspace_size(batch, Hq, Hkv, d, B, topk,
+                                                         max_blocks)) > 0:
+        own.append(workspace := torch.empty(ws_bytes, dtype=torch.uint8, device=q.device))
+        at = workspace.data_ptr()
     status = load_library().ssa_decode_paged_q8(
         q.data_ptr(), _dtype_code(q), Kp.data_ptr(), Ks.data_ptr(), Vp.data_ptr(), Vs.data_ptr(),
         fmt, None if S is None else S.data_ptr(), page_table.data_ptr(), max_blocks, num_pages,
         seqlens.data_ptr(), batch, Hq, Hkv, d, B, topk, d ** -0.5 if scale is None else scale,
-        O.data_ptr(), None if idx is None else idx.data_ptr(), workspace.data_ptr(),
-        workspace.numel(), _launch_on(stream, dev, own))
+        O.data_ptr(), None if idx is None else idx.data_ptr(), at, ws_bytes,
+        _launch_on(stream, dev, own))
     _check("ssa_decode_paged_q8", status)
     return O, idx
 

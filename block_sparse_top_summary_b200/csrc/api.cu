@@ -464,7 +464,7 @@ ssa_status ssa_decode_paged_q8_workspace_size(int batch, int Hq, int Hkv, int d,
   ssa_status st = check_q8(d, B, SSA_E4M3, SSA_BF16, Hkv, max_blocks, 1);
   if (st != SSA_OK) return st;
   if (batch <= 0 || Hq <= 0 || topk < 0 || Hq % Hkv != 0) return SSA_ERR_INVALID_ARG;
-  *bytes = ssa::plan_q8(batch, Hq, Hkv, d, topk, max_blocks).bytes;
+  *bytes = ssa::plan_q8(batch, Hq, Hkv, d, B, topk, max_blocks).bytes;
   return SSA_OK;
 }
 
@@ -485,7 +485,7 @@ ssa_status ssa_decode_paged_q8(const void* q, ssa_dtype dtype, const void* Kp, c
     return SSA_ERR_UNSUPPORTED;
   if (!(scale > 0.f)) return SSA_ERR_INVALID_ARG;
   if (q == nullptr || Kp == nullptr || Ks == nullptr || Vp == nullptr || Vs == nullptr ||
-      page_table == nullptr || seqlens == nullptr || O == nullptr || workspace == nullptr)
+      page_table == nullptr || seqlens == nullptr || O == nullptr)
     return SSA_ERR_INVALID_ARG;
   if (S == nullptr && topk < max_blocks - 2) return SSA_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(Kp) || !aligned16(Ks) || !aligned16(Vp) || !aligned16(Vs) ||
@@ -493,8 +493,8 @@ ssa_status ssa_decode_paged_q8(const void* q, ssa_dtype dtype, const void* Kp, c
       !aligned16(idx))
     return SSA_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return SSA_ERR_INVALID_ARG;
-  const ssa::Q8Plan p = ssa::plan_q8(batch, Hq, Hkv, d, topk, max_blocks);
-  if (ws_bytes < p.bytes) return SSA_ERR_INVALID_ARG;
+  const ssa::Q8Plan p = ssa::plan_q8(batch, Hq, Hkv, d, B, topk, max_blocks);
+  if (ws_bytes < p.bytes || (p.bytes > 0 && workspace == nullptr)) return SSA_ERR_INVALID_ARG;
   return from_cuda(ssa::launch_decode_q8(p, q, Kp, Ks, Vp, Vs, fmt, dtype, S, page_table,
                                          max_blocks, num_pages, seqlens, batch, Hq, Hkv, d, B,
                                          scale, O, idx, workspace,

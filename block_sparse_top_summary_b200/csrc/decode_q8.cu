@@ -47,7 +47,8 @@ namespace {
 constexpr int kQW = 12;                 // warps of the split kernel
 constexpr int kQThreads = 32 * kQW;
 constexpr int kSlice = 16;              // keys a slice
-constexpr int kWholeSlices = 96;        // most slices of a pair that a block takes whole
+constexpr int kWholeSlices = 96;        // most slices of a pair that a block takes whole,
+constexpr size_t kWholePairs = 148;     // and most pairs then
 constexpr int kQGridMax = 160;          // most blocks of the split grid (148 SMs, one each)
 // Slices in flight or in use a warp: 144 KB (d = 128) or 192 KB (d = 64) a block.
 __host__ __device__ constexpr int q8_stages(int d) { return d == 128 ? 3 : 8; }
@@ -1031,7 +1032,7 @@ __global__ void __launch_bounds__(kQThreads, 1) q8_split_kernel(
   }
 }
 
-Q8Plan plan_q8(int batch, int Hq, int Hkv, int d, int topk, int max_blocks) {
+Q8Plan plan_q8(int batch, int Hq, int Hkv, int d, int B, int topk, int max_blocks) {
   Q8Plan p{};
   p.kk = topk < max_blocks ? topk : max_blocks;
   p.width = p.kk + 2;
@@ -1040,6 +1041,14 @@ Q8Plan plan_q8(int batch, int Hq, int Hkv, int d, int topk, int max_blocks) {
   // lists are kept for rows that leave blocks out; with topk >= the candidates of
   // the longest row there are none
   p.lists = topk < max_blocks - 2;
+  // Few pairs of few slices go to a block each (of 148 SMs) and need no split: without
+  // lists in one launch and without scratch.  Split and whole, us: 1 row of 100 tokens
+  // (8 / 2 heads) 10.3, 8.2; of 777 (4 / 1) 14.3, 12.3; 16 rows of 1500 (32 / 8) 21.5, 16.4;
+  // 24 ragged rows, top-8 blocks of 128 (8 / 4) 25.6, 22.6; but 1 row of 3000 (8 pairs)
+  // 16.4, 22.5 and 64 rows of 1500 (512 pairs) 46.6, 59.4.
+  const int most = max_blocks < p.width ? max_blocks : p.width;  // blocks of a pair
+  p.whole = pairs <= kWholePairs && (long long)most * (B / kSlice) <= kWholeSlices;
+  if (p.whole && !p.lists) return p;  // bytes = 0
   p.off_off = up(p.lists ? pairs * p.width * sizeof(int32_t) : 0);
   p.off_ctr = up(p.off_off + ((size_t)batch + 1) * sizeof(int32_t));
   p.off_part = up(p.off_ctr + pairs * sizeof(int));
@@ -1086,14 +1095,7 @@ static cudaError_t launch_q8_t(const Q8Plan& p, const void* q, const void* Kp, c
                               (const int32_t*)ws_off, ws_part, ws_ctr, (T*)O,
                               scale * 1.4426950408889634f);
   };
-  // Few pairs of few slices go to a block each and need no split: without lists in
-  // one launch.  Split and whole, us: 1 row of 100 tokens (8 / 2 heads) 10.3, 8.2; of 777
-  // (4 / 1) 14.3, 12.3; 16 rows of 1500 (32 / 8) 21.5, 16.4; 24 ragged rows, top-8 blocks of
-  // 128 (8 / 4) 25.6, 22.6; but 1 row of 3000 (8 pairs) 16.4, 22.5 and 64 rows of 1500
-  // (512 pairs) 46.6, 59.4.
-  const int most = max_blocks < p.width ? max_blocks : p.width;  // blocks of a pair
-  const bool whole = batch * (long long)Hkv <= sms && most * (B / kSlice) <= kWholeSlices;
-  if (whole && !p.lists) return split((unsigned)(batch * Hkv), true);
+  if (p.whole && !p.lists) return split((unsigned)(batch * Hkv), true);
 
   // Few pairs of long rows: several blocks score a pair's summaries, as many as
   // the GPU takes at once (2 an SM) and as leave each warp two steps of 16.
@@ -1119,8 +1121,8 @@ static cudaError_t launch_q8_t(const Q8Plan& p, const void* q, const void* Kp, c
   attr = cudaLaunchAttribute{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
-  return whole ? split((unsigned)(batch * Hkv), true)
-               : split((unsigned)(sms < kQGridMax ? sms : kQGridMax), false);
+  return p.whole ? split((unsigned)(batch * Hkv), true)
+                 : split((unsigned)(sms < kQGridMax ? sms : kQGridMax), false);
 }
 
 cudaError_t launch_decode_q8(const Q8Plan& p, const void* q, const void* Kp, const float* Ks,

@@ -133,10 +133,11 @@ struct Q8Plan {
   int kk;     // effective top-k: min(topk, max_blocks)
   int width;  // idx row width: kk + 2
   bool lists;  // whether a row can leave blocks out
-  // scratch: block lists (from 0), slices before each sequence, arrivals, partial records
+  bool whole;  // whether a pair is one block's work
+  // scratch (none where whole and no lists): block lists (from 0), slices before each sequence, arrivals, partial records
   size_t off_off, off_ctr, off_part, bytes;
 };
-Q8Plan plan_q8(int batch, int Hq, int Hkv, int d, int topk, int max_blocks);
+Q8Plan plan_q8(int batch, int Hq, int Hkv, int d, int B, int topk, int max_blocks);
 cudaError_t launch_decode_q8(const Q8Plan& p, const void* q, const void* Kp, const float* Ks,
                              const void* Vp, const float* Vs, ssa_qformat fmt, ssa_dtype dt,
                              const float* S, const int32_t* table, int max_blocks, int num_pages,

@@ -505,7 +505,8 @@ ssa_status ssa_append_paged_q8(void* Kp, float* Ks, void* Vp, float* Vs, ssa_qfo
  * [1, max_blocks * B] writes zeros, and -1 to its idx rows).
  * workspace: >= ssa_decode_paged_q8_workspace_size(...) bytes, 256-byte aligned,
  * contents on entry ignored; calls that share one must not overlap on the
- * device.  Hq / Hkv <= 8; max_blocks <= 16384.
+ * device.  The size is 0, and the workspace may be NULL, for a few short rows
+ * read whole.  Hq / Hkv <= 8; max_blocks <= 16384.
  */
 ssa_status ssa_decode_paged_q8_workspace_size(int batch, int Hq, int Hkv, int d, int B, int topk,
                                               int max_blocks, size_t* bytes);

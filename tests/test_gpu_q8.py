@@ -151,11 +151,12 @@ def test_tensors_of_another_kind_are_refused(ssa):
                 dict(K=K.view(torch.uint8)), dict(Ks=Ks.double()), dict(O=torch.empty_like(q).bfloat16())):
         with pytest.raises(TypeError):
             call(**bad)
-    with pytest.raises(ssa.SSAError):
-        call(workspace=torch.empty(64, dtype=torch.uint8, device=DEV))
+    wide = torch.zeros(1, 9, dtype=torch.int32, device=DEV)
+    with pytest.raises(ssa.SSAError):  # too small a workspace
+        ssa.ssa_decode_paged_q8(q, K, Ks, V, Vs, torch.zeros(1, 2, 9, d, device=DEV), wide, lens, B,
+                                2, workspace=torch.empty(64, dtype=torch.uint8, device=DEV))
     with pytest.raises(ssa.SSAError):  # no summaries, and blocks to choose from
-        ssa.ssa_decode_paged_q8(q, K, Ks, V, Vs, None, torch.zeros(1, 9, dtype=torch.int32,
-                                                                   device=DEV), lens, B, 2)
+        ssa.ssa_decode_paged_q8(q, K, Ks, V, Vs, None, wide, lens, B, 2)
     with pytest.raises(TypeError):
         ssa.ssa_page_plan(lens.long(), lens, table, lens, lens, B, 4)
     torch.cuda.synchronize()

@@ -94,7 +94,11 @@ def test_decode_q8_rejections(lib):
     f = lib.ssa_decode_paged_q8_workspace_size
     assert f(2, 7, 2, 128, 64, 4, 64, ctypes.byref(n)) == 1
     assert f(2, 8, 2, 128, 64, 4, 64, NULL) == 1
-    # lists are kept only where blocks can be left out
+    # a few short rows read whole need none; lists are kept only where blocks can be left out
+    assert abi.ssa_decode_paged_q8_workspace_size(2, 8, 2, 128, 64, 62, 24) == 0
+    assert abi.ssa_decode_paged_q8_workspace_size(2, 8, 2, 128, 64, 62, 25) > 0
+    assert abi.ssa_decode_paged_q8_workspace_size(75, 8, 2, 128, 64, 62, 24) > 0
+    assert abi.ssa_decode_paged_q8_workspace_size(2, 8, 2, 128, 64, 4, 24) > 0
     assert abi.ssa_decode_paged_q8_workspace_size(64, 32, 8, 128, 64, 1 << 30, 16384) < 16 << 20
 
 
