@@ -569,15 +569,14 @@ def ssa_page_plan(have, want, page_table, ring, pool, B: int, max_new: int, keep
     if got is not None or cu is not None or slots is not None or pool_out is not None:
         _refuse(dev, ("got", got, i32, rows), ("cu", cu, i32, (batch + 1,)),
                 ("slots", slots, i32, (max_new,)), ("pool_out", pool_out, i32, two))
-    at = have.device
-    if got is None:
-        own.append(got := torch.empty(batch, dtype=i32, device=at))
-    if cu is None:
-        own.append(cu := torch.empty(batch + 1, dtype=i32, device=at))
-    if slots is None:
-        own.append(slots := torch.empty(max_new, dtype=i32, device=at))
-    if pool_out is None:
-        own.append(pool_out := torch.empty(2, dtype=i32, device=at))
+    if got is None or cu is None or slots is None or pool_out is None:
+        # the outputs that are not given, in one allocation
+        own.append(torch.empty(max_new + 2 * batch + 3, dtype=i32, device=have.device))
+        new = own[0].split_with_sizes((max_new, batch, batch + 1, 2))
+        slots = new[0] if slots is None else slots
+        got = new[1] if got is None else got
+        cu = new[2] if cu is None else cu
+        pool_out = new[3] if pool_out is None else pool_out
     status = load_library().ssa_page_plan(
         have.data_ptr(), want.data_ptr(), None if keep is None else keep.data_ptr(), batch, B,
         page_table.data_ptr(), max_blocks, num_pages, ring.data_ptr(), pool.data_ptr(),

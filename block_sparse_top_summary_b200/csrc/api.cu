@@ -7,6 +7,7 @@
 namespace {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 bool dtype_ok(ssa_dtype dt) { return dt == SSA_F32 || dt == SSA_BF16; }
 
@@ -422,9 +423,9 @@ ssa_status ssa_page_plan(const int32_t* have, const int32_t* want, const int32_t
       pool == nullptr || pool_out == nullptr || got == nullptr || cu == nullptr ||
       (max_new > 0 && slots == nullptr))
     return SSA_ERR_INVALID_ARG;
-  if (!aligned16(have) || !aligned16(want) || !aligned16(keep) || !aligned16(page_table) ||
-      !aligned16(ring) || !aligned16(pool) || !aligned16(pool_out) || !aligned16(got) ||
-      !aligned16(cu) || !aligned16(slots))
+  if (!aligned4(have) || !aligned4(want) || !aligned4(keep) || !aligned4(page_table) ||
+      !aligned4(ring) || !aligned4(pool) || !aligned4(pool_out) || !aligned4(got) ||
+      !aligned4(cu) || !aligned16(slots))
     return SSA_ERR_INVALID_ARG;
   return from_cuda(ssa::launch_page_plan(have, want, keep, batch, B, page_table, max_blocks,
                                          num_pages, ring, pool, pool_out, got, cu, slots, max_new,
@@ -445,8 +446,8 @@ ssa_status ssa_append_paged_q8(void* Kp, float* Ks, void* Vp, float* Vs, ssa_qfo
   if (Kp == nullptr || Ks == nullptr || Vp == nullptr || Vs == nullptr || slots == nullptr ||
       cu == nullptr || seqlens == nullptr || k_new == nullptr || v_new == nullptr)
     return SSA_ERR_INVALID_ARG;
-  if (!aligned16(Kp) || !aligned16(Ks) || !aligned16(Vp) || !aligned16(Vs) || !aligned16(S) ||
-      !aligned16(slots) || !aligned16(cu) || !aligned16(seqlens) || !aligned16(k_new) ||
+  if (!aligned16(Kp) || !aligned4(Ks) || !aligned16(Vp) || !aligned4(Vs) || !aligned16(S) ||
+      !aligned4(slots) || !aligned4(cu) || !aligned4(seqlens) || !aligned16(k_new) ||
       !aligned16(v_new))
     return SSA_ERR_INVALID_ARG;
   const int epc = dtype == SSA_BF16 ? 8 : 4;  // elements of 16 bytes
@@ -488,9 +489,9 @@ ssa_status ssa_decode_paged_q8(const void* q, ssa_dtype dtype, const void* Kp, c
       page_table == nullptr || seqlens == nullptr || O == nullptr)
     return SSA_ERR_INVALID_ARG;
   if (S == nullptr && topk < max_blocks - 2) return SSA_ERR_INVALID_ARG;
-  if (!aligned16(q) || !aligned16(Kp) || !aligned16(Ks) || !aligned16(Vp) || !aligned16(Vs) ||
-      !aligned16(S) || !aligned16(page_table) || !aligned16(seqlens) || !aligned16(O) ||
-      !aligned16(idx))
+  if (!aligned16(q) || !aligned16(Kp) || !aligned4(Ks) || !aligned16(Vp) || !aligned4(Vs) ||
+      !aligned16(S) || !aligned4(page_table) || !aligned4(seqlens) || !aligned16(O) ||
+      !aligned4(idx))
     return SSA_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return SSA_ERR_INVALID_ARG;
   const ssa::Q8Plan p = ssa::plan_q8(batch, Hq, Hkv, d, B, topk, max_blocks);

@@ -439,6 +439,8 @@ ssa_status ssa_decode_append_paged(void* Kp, void* Vp, ssa_dtype dtype, float* S
  * hold gets slots of -1 for that block's tokens or for all of its tokens.
  * All int32: have, want, keep, got: [batch]; page_table: [batch, max_blocks];
  * ring: [num_pages]; pool, pool_out: [2]; cu: [batch + 1]; slots: [max_new].
+ * Here and in the two calls below, int32 arrays and scales need no more than their own
+ * alignment, but for slots (16 bytes, as written here).
  * got may be have, and pool_out may be pool; nothing else may overlap.
  * slots may be NULL when max_new is 0.  Supported: B a multiple of 16 in
  * [16, 128]; batch <= 8192; max_new <= 2^30; max_blocks * B and num_pages * B

@@ -13,6 +13,7 @@ from block_sparse_top_summary_b200 import abi
 NULL = None
 FAKE = ctypes.c_void_p(0x100000)  # never dereferenced
 ODD = ctypes.c_void_p(0x100008)
+ODD2 = ctypes.c_void_p(0x100002)
 
 
 @pytest.fixture(scope="module")
@@ -37,8 +38,8 @@ def test_page_plan_rejections(lib):
                     NULL])
     for n in ("have", "want", "table", "ring", "pool", "pool_out", "got", "cu", "slots"):
         assert call(**{n: NULL}) == 1, n
-        assert call(**{n: ODD}) == 1, n
-    assert call(keep=ODD) == 1
+        assert call(**{n: ODD2}) == 1, n
+    assert call(keep=ODD2) == 1 and call(slots=ODD) == 1
     assert call(batch=0) == 1 and call(max_blocks=0) == 1 and call(num_pages=0) == 1
     assert call(max_new=-1) == 1 and call(B=0) == 1
     assert call(B=40) == 2 and call(B=144) == 2
@@ -55,6 +56,8 @@ def test_append_q8_rejections(lib):
                     8, 2, 128, 64, 16, 32, NULL])
     for n in ("Kp", "Ks", "Vp", "Vs", "slots", "cu", "seqlens", "k", "v"):
         assert call(**{n: NULL}) == 1, n
+        assert call(**{n: ODD2}) == 1, n
+    for n in ("Kp", "Vp", "k", "v"):
         assert call(**{n: ODD}) == 1, n
     assert call(S=ODD) == 1
     assert call(fmt=2) == 1 and call(dt=7) == 1
@@ -79,9 +82,11 @@ def test_decode_q8_rejections(lib):
                     64, 4, 0.088, FAKE, NULL, FAKE, need, NULL])
     for n in ("q", "Kp", "Ks", "Vp", "Vs", "S", "table", "seqlens", "O", "ws"):
         assert call(**{n: NULL}) == 1, n
+        assert call(**{n: ODD2}) == 1, n
+    for n in ("q", "Kp", "Vp", "S", "O", "ws"):
         assert call(**{n: ODD}) == 1, n
     assert call(S=NULL, topk=61) == 1         # 62 candidates at most
-    assert call(idx=ODD) == 1
+    assert call(idx=ODD2) == 1
     assert call(ws=ctypes.c_void_p(0x100010)) == 1
     assert call(ws_bytes=need - 1) == 1
     assert call(fmt=2) == 1 and call(dt=2) == 1
