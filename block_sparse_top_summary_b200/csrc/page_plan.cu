@@ -33,6 +33,7 @@ namespace {
 
 constexpr int kPlanThreads = 1024;
 constexpr int kIntMax = 0x7fffffff;
+constexpr int kLongRow = 2048;  // most pages that a warp moves for one row
 
 struct PlanRow {
   long long n, need, back;
@@ -150,7 +151,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(
   int* from = row + batch;    // [batch] first block a shrinking row gives back
   int* len = from + batch;    // [batch] got
   __shared__ PlanRow wsum[32];
-  __shared__ int s_taken;
+  __shared__ int s_taken, s_long;
   const int t = threadIdx.x;
   const int blocks = gridDim.x, rank = blockIdx.x;  // one cluster
   if (!kSlots) grid_launch_next();
@@ -159,7 +160,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(
   // a pool state out of range is taken as an empty or a full ring
   const int head = min(max(pool[0], 0), num_pages - 1);
   const int count = min(max(pool[1], 0), num_pages);
-  if (t == 0) s_taken = 0;
+  if (t == 0) s_taken = s_long = 0;
 
   const int per = (batch + kPlanThreads - 1) / kPlanThreads;
   const int r0 = min(t * per, batch), r1 = min(r0 + per, batch);
@@ -203,6 +204,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(
     const bool grows = r.v.n > 0 && run.n <= (long long)max_new &&
                        (r.v.need == 0 || run.need <= (long long)count);
     if (grows && r.v.need > 0) taken = (int)run.need;
+    if (r.v.need > kLongRow || r.v.back > kLongRow) s_long = 1;
     tok[b] = clamp_int(run.n);
     pag[b] = clamp_int(run.need);
     bak[b] = clamp_int(run.back);
@@ -253,22 +255,37 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(
       if (tok[b] > i && i < tokens) slots[i] = slot_at(b, row[b], i);
     }
   }
-  // new blocks' pages
-  for (int w0 = rank * kPlanThreads + t - lane; w0 < taken; w0 += blocks * kPlanThreads) {
-    const int i = min(w0 + lane, taken - 1);
-    const int page = ring[ring_at(i)];
-    const int b = row_above_warp(pag, batch, i, w0, min(w0 + 32, taken) - 1);
-    const int hb = div.up(row[b] & kIntMax);
-    if (w0 + lane < taken)
-      table[(int64_t)b * max_blocks + hb + i - (b > 0 ? pag[b - 1] : 0)] = page;
+  // New blocks' pages, and returned pages behind the free ones (the entries taken above
+  // are not reached, as at most num_pages - count come back): one or two pages of a row
+  // by a thread, more by a warp, and more than kLongRow by all threads together.
+  auto move = [&](int b, int first, int step) {
+    const int p0 = b > 0 ? pag[b - 1] : 0, k0 = b > 0 ? bak[b - 1] : 0;
+    int32_t* const mine = table + (int64_t)b * max_blocks;
+    if (row[b] < 0) {
+      int32_t* const to = mine + div.up(row[b] & kIntMax);
+#pragma unroll 4
+      for (int i = first; i < pag[b] - p0; i += step) to[i] = ring[ring_at(p0 + i)];
+    }
+    const int n = min(bak[b], given) - k0;
+#pragma unroll 4
+    for (int i = first; i < n; i += step) ring[ring_at(count + k0 + i)] = mine[from[b] + i];
+  };
+  const int warps = blocks * (kPlanThreads / 32), w = rank * (kPlanThreads / 32) + (t >> 5);
+  for (int k = 0; w + k * warps < batch; k += 32) {
+    const int b = w + (k + lane) * warps;
+    const int n = b < batch ? max(pag[b] - (b > 0 ? pag[b - 1] : 0),
+                                  bak[b] - (b > 0 ? bak[b - 1] : 0))
+                            : 0;
+    if (n > 0 && n <= 2) move(b, 0, 1);
+    for (uint32_t m = __ballot_sync(0xffffffffu, n > 2 && n <= kLongRow); m != 0; m &= m - 1)
+      move(w + (k + __ffs(m) - 1) * warps, lane, 32);
   }
-  // returned pages go behind the free ones; entries taken above are not reached,
-  // as at most num_pages - count come back
-  for (int w0 = rank * kPlanThreads + t - lane; w0 < given; w0 += blocks * kPlanThreads) {
-    const int i = min(w0 + lane, given - 1);
-    const int b = row_above_warp(bak, batch, i, w0, min(w0 + 32, given) - 1);
-    const int page = table[(int64_t)b * max_blocks + from[b] + i - (b > 0 ? bak[b - 1] : 0)];
-    if (w0 + lane < given) ring[ring_at(count + i)] = page;
+  for (int b0 = 0; s_long && b0 < batch; b0 += 32) {
+    const int b = b0 + lane;
+    const bool lng = b < batch && (pag[b] - (b > 0 ? pag[b - 1] : 0) > kLongRow ||
+                                   bak[b] - (b > 0 ? bak[b - 1] : 0) > kLongRow);
+    for (uint32_t m = __ballot_sync(0xffffffffu, lng); m != 0; m &= m - 1)
+      move(b0 + __ffs(m) - 1, rank * kPlanThreads + t, blocks * kPlanThreads);
   }
   if (!kSlots) cluster_wait();
   if (rank > 0) return;
@@ -282,7 +299,9 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(
 
 // The slots of granted rows from what page_plan_kernel has written: lengths, prefix
 // sums, page table and the first slot of each row (-1: refused).  Another warp may be
-// writing that one again, with the same value.  A warp takes 256 slots on end.
+// writing that one again, with the same value.  A warp takes 256 slots on end; its
+// time is a chain of dependent reads: prefix sums (two or three steps of 32 guesses,
+// for its first and last token at once), rows, first slots, pages.
 __global__ void __launch_bounds__(256) page_slots_kernel(const int32_t* __restrict__ got,
                                                          const int32_t* __restrict__ cu,
                                                          const int32_t* __restrict__ table,
@@ -293,24 +312,48 @@ __global__ void __launch_bounds__(256) page_slots_kernel(const int32_t* __restri
   const int w0 = (blockIdx.x * 8 + (threadIdx.x >> 5)) * 256;
   const BlockDiv div(B);
   grid_wait();
-  const int tokens = cu[batch];
   if (w0 >= max_new) return;
+  const int tokens = cu[batch];
   const int last = min(w0 + 256, tokens) - 1;
-  int lo = 0, hi = 0;
-  if (w0 < tokens) {
-    lo = find_row(cu + 1, 0, batch, w0);
-    hi = cu[lo + 1] > last ? lo : find_row(cu + 1, lo, batch - lo, last);
+  // the first row whose sum lies above x, for x = w0 and x = last
+  int at[2] = {0, 0}, len[2] = {batch, batch};
+  while (w0 < tokens && max(len[0], len[1]) > 1) {
+    int step[2], sum[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      step[e] = (len[e] + 31) / 32;
+      sum[e] = cu[1 + at[e] + min((lane + 1) * step[e], len[e]) - 1];
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int k = __ffs(__ballot_sync(0xffffffffu, sum[e] > (e == 0 ? w0 : last))) - 1;
+      at[e] += k * step[e];
+      len[e] = min(step[e], len[e] - k * step[e]);
+    }
+  }
+  const int lo = at[0], rows = at[1] - at[0] + 1;
+  // lane r holds row lo + r: first token, end, position of the first token, granted or not
+  int c = 0, end = 0, p0 = 0;
+  bool granted = false;
+  if (w0 < tokens && lane < rows) {
+    c = cu[lo + lane];
+    end = cu[lo + lane + 1];
+    p0 = got[lo + lane] - (end - c);
+    granted = end > c && slots[c] >= 0;
   }
   auto slot_of = [&](int page, int r) {
     return page >= 0 && page < num_pages ? page * B + r : -1;
   };
-  if (lo == hi && last == w0 + 255) {
+  if (rows == 1 && last == w0 + 255) {
     // one row: 8 slots on end a thread, in at most two blocks (B >= 16)
-    const int c = cu[lo], p0 = got[lo] - (cu[lo + 1] - c), i0 = w0 + lane * 8;
+    c = __shfl_sync(0xffffffffu, c, 0);
+    p0 = __shfl_sync(0xffffffffu, p0, 0);
+    granted = __shfl_sync(0xffffffffu, granted, 0);
+    const int i0 = w0 + lane * 8;
     int out[8];
 #pragma unroll
     for (int u = 0; u < 8; ++u) out[u] = -1;
-    if (slots[c] >= 0) {
+    if (granted) {
       const int pos = p0 + i0 - c, j = div(pos), r = pos - j * B, left = B - r;
       const int32_t* w = table + (int64_t)lo * max_blocks + j;
       const int a = w[0], z = left < 8 ? w[1] : a;
@@ -321,15 +364,40 @@ __global__ void __launch_bounds__(256) page_slots_kernel(const int32_t* __restri
     *reinterpret_cast<int4*>(slots + i0 + 4) = make_int4(out[4], out[5], out[6], out[7]);
     return;
   }
+  if (rows <= 32) {
+    // row of token w0 + 32 u + lane: those that end before it are counted
+    int k[8] = {0, 0, 0, 0, 0, 0, 0, 0}, out[8];
+    for (int r = 0; r < rows - 1; ++r) {
+      const int e = __shfl_sync(0xffffffffu, end, r);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) k[u] += e <= w0 + 32 * u + lane;
+    }
+    int place[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int i = w0 + 32 * u + lane;
+      const int first = __shfl_sync(0xffffffffu, c, k[u]), p = __shfl_sync(0xffffffffu, p0, k[u]);
+      const bool ok = __shfl_sync(0xffffffffu, granted, k[u]) && i < tokens;
+      const int pos = p + i - first, j = ok ? div(pos) : 0;
+      place[u] = pos - j * B;
+      out[u] = ok ? table[(int64_t)(lo + k[u]) * max_blocks + j] : -1;
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int i = w0 + 32 * u + lane;
+      if (i < max_new) slots[i] = slot_of(out[u], place[u]);
+    }
+    return;
+  }
 #pragma unroll 4
   for (int u = 0; u < 8; ++u) {
     const int i = w0 + 32 * u + lane;
     int slot = -1;
     if (i < tokens) {
-      const int b = lo + row_above(cu + 1 + lo, hi - lo + 1, i);
-      const int c = cu[b];
-      if (slots[c] >= 0) {
-        const int pos = got[b] - (cu[b + 1] - c) + i - c, j = div(pos);
+      const int b = lo + row_above(cu + 1 + lo, rows, i);
+      const int f = cu[b];
+      if (slots[f] >= 0) {
+        const int pos = got[b] - (cu[b + 1] - f) + i - f, j = div(pos);
         slot = slot_of(table[(int64_t)b * max_blocks + j], pos - j * B);
       }
     }

@@ -96,9 +96,11 @@ def test_plan_matches_the_oracle(ssa, n, B, mb, in_place):
 
 
 @pytest.mark.parametrize("n,B,mb,prompt", [(40, 16, 64, 1000), (700, 48, 20, 90),
-                                           (9, 128, 40, 5000), (3000, 32, 3, 30)])
+                                           (9, 128, 40, 5000), (3000, 32, 3, 30),
+                                           (7, 16, 5000, 70000)])
 def test_plan_of_many_tokens(ssa, n, B, mb, prompt):
-    # more than 8192 slots: a cluster, 8 tokens a thread; short and long rows, refused ones
+    # more than 8192 slots: a cluster and a kernel for the slots; short and long rows, up to
+    # thousands of pages; refused ones
     for seed in range(2):
         have, want, keep, table, ring, (head, count) = _plan_case(n, B, mb, seed + n, prompt=prompt)
         total = int(np.maximum(want - have, 0).sum())
