@@ -20,9 +20,9 @@
 // slot, which want the whole GPU.  So up to 8192 slots one block does it all, and
 // beyond a cluster of 8 does rows and pages (all of its blocks form the sums, and a
 // cluster barrier stands before the last writes) and a second kernel the slots.
-// Cluster and slots kernel against one block, us: 256 rows of 1 token 16.1, 6.2; 4000
-// rows of 1 24.4, 14.4; 8 rows of 1000 10.3, 10.3; 64 rows of 250 10.3, 16.4; 4 rows of 8000
-// 10.3, 24.6.  0.47 million slots of 1024 rows with 31 thousand pages: 21 us; with
+// Cluster and slots kernel against one block, us: 256 rows of 1 token 16.4, 6.1; 4000
+// rows of 1 24.3, 14.3; 8 rows of 1000 8.2, 9.1; 64 rows of 250 10.2, 16.4; 4 rows of 8000
+// 10.2, 24.6.  0.47 million slots of 1024 rows with 31 thousand pages: 18 us; with
 // the slots in the cluster 31 us, in one block 637 us.
 #include "common.cuh"
 #include "kernels.h"
@@ -271,14 +271,16 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(
     for (int i = first; i < n; i += step) ring[ring_at(count + k0 + i)] = mine[from[b] + i];
   };
   const int warps = blocks * (kPlanThreads / 32), w = rank * (kPlanThreads / 32) + (t >> 5);
-  for (int k = 0; w + k * warps < batch; k += 32) {
-    const int b = w + (k + lane) * warps;
+  // lane l of warp w takes the rows (k + l) warps + (w + l) % warps: no two lanes in a bank
+  auto row_at = [&](int k, int l) { return (k + l) * warps + ((w + l) & (warps - 1)); };
+  for (int k = 0; k * warps < batch; k += 32) {
+    const int b = row_at(k, lane);
     const int n = b < batch ? max(pag[b] - (b > 0 ? pag[b - 1] : 0),
                                   bak[b] - (b > 0 ? bak[b - 1] : 0))
                             : 0;
     if (n > 0 && n <= 2) move(b, 0, 1);
     for (uint32_t m = __ballot_sync(0xffffffffu, n > 2 && n <= kLongRow); m != 0; m &= m - 1)
-      move(w + (k + __ffs(m) - 1) * warps, lane, 32);
+      move(row_at(k, __ffs(m) - 1), lane, 32);
   }
   for (int b0 = 0; s_long && b0 < batch; b0 += 32) {
     const int b = b0 + lane;
