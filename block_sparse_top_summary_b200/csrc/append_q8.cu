@@ -116,6 +116,7 @@ __global__ void __launch_bounds__(512) append_q8_kernel(
   const bool is_v = blockIdx.y & 1;
   const int g0 = (blockIdx.y >> 1) * heads, g1 = min(g0 + heads, Hkv);
   const int u = blockIdx.x;
+  grid_wait();  // the kernels before
 
   // the sequence: the last b with floor(cu[b] / B) + 2 b <= u, 32 guesses a step
   int b = 0;
@@ -339,10 +340,19 @@ static cudaError_t launch_append_q8_t(void* Kp, float* Ks, void* Vp, float* Vs, 
         append_q8_kernel<T, D, F>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
   }
-  append_q8_kernel<T, D, F><<<grid, threads, smem, st>>>(
-      (uint8_t*)Kp, Ks, (uint8_t*)Vp, Vs, S, slots, cu, seqlens, (const T*)kn, (const T*)vn,
-      tok_stride, head_stride, batch, T_max, Hkv, heads, B, max_blocks, num_pages);
-  return cudaGetLastError();
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, append_q8_kernel<T, D, F>, (uint8_t*)Kp, Ks, (uint8_t*)Vp, Vs, S,
+                            slots, cu, seqlens, (const T*)kn, (const T*)vn, tok_stride,
+                            head_stride, batch, T_max, Hkv, heads, B, max_blocks, num_pages);
 }
 
 cudaError_t launch_append_q8(void* Kp, float* Ks, void* Vp, float* Vs, ssa_qformat fmt, float* S,

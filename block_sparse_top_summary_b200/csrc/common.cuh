@@ -83,8 +83,11 @@ __device__ __forceinline__ uint32_t lanemask_lt() {
   return m;
 }
 
-// Programmatic dependent launch: a kernel lets the next one of its stream start, and
-// that one waits here until the first has ended and its writes are visible.
+// Programmatic dependent launch.  A kernel launched with that attribute may start when
+// the one before it in its stream says so, or else at that one's end, and waits here
+// until the one before has ended and its writes are visible.  A kernel calls
+// grid_launch_next only behind its own grid_wait, so that whatever starts by it
+// finds all earlier kernels ended too.
 __device__ __forceinline__ void grid_launch_next() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }

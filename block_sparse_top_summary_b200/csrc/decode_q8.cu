@@ -302,6 +302,7 @@ __global__ void __launch_bounds__(256, 4) q8_route_kernel(
   __shared__ int sbuf[16];
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const int bg = blockIdx.x / CS, rank = blockIdx.x - bg * CS;
+  grid_wait();         // the kernels before
   grid_launch_next();  // the split kernel's blocks may come in as these leave
   if (bg == batch * Hkv) {
     if (rank > 0) return;
@@ -448,6 +449,7 @@ __global__ void __launch_bounds__(kQThreads, 1) q8_split_kernel(
 
   const int G = Hq / Hkv, spb = B / kSlice;
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  if (whole_pairs && !lists) grid_wait();  // the kernels before (there is no route kernel)
   // Slices of the sequences before each, per KV head: formed here up to kQThreads
   // sequences, so that only block lists (where there are any) are waited for.
   const int32_t* off = ws_off;
@@ -1080,10 +1082,13 @@ static cudaError_t launch_q8_t(const Q8Plan& p, const void* q, const void* Kp, c
   e = cudaFuncSetAttribute(q8_split_kernel<T, D, F>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            (int)smem2);
   if (e != cudaSuccess) return e;
-  cudaLaunchAttribute attr{};
+  cudaLaunchAttribute attr[2] = {};
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
   cfg.stream = st;
-  cfg.attrs = &attr;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
   auto split = [&](unsigned grid, bool whole) {
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(kQThreads);
@@ -1107,20 +1112,18 @@ static cudaError_t launch_q8_t(const Q8Plan& p, const void* q, const void* Kp, c
                              (int)smem1);
     if (e != cudaSuccess) return e;
   }
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = CS;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = CS;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.gridDim = dim3((unsigned)(batch * Hkv + 1) * CS);
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = smem1;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   e = cudaLaunchKernelEx(&cfg, q8_route_kernel<T, D>, (const T*)q, S, seqlens, batch, Hq, Hkv,
                          max_blocks * B, B, max_blocks, p.kk, p.width, CS, ws_idx, ws_ctr, ws_off,
                          (T*)O, idx_out, 1.0f / sqrtf((float)D));
   if (e != cudaSuccess) return e;
-  attr = cudaLaunchAttribute{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.numAttrs = 1;
   return p.whole ? split((unsigned)(batch * Hkv), true)
                  : split((unsigned)(sms < kQGridMax ? sms : kQGridMax), false);
 }

@@ -40,7 +40,8 @@ struct PlanRow {
 };
 
 // x / B for 0 <= x < 2^31, B = 16 d with d <= 8: with m = floor(2^32 / d) + 1 and
-// n = x / 16 < 2^27, n m / 2^32 is less than n d / 2^32 < 1 / d above n / d.
+// n = x / 16 < 2^27, n m / 2^32 is at most n / 2^32 < 1 / 32 above n / d, so its whole
+// part is that of n / d.
 struct BlockDiv {
   int B;
   uint32_t m;
@@ -154,6 +155,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(
   __shared__ int s_taken, s_long;
   const int t = threadIdx.x;
   const int blocks = gridDim.x, rank = blockIdx.x;  // one cluster
+  grid_wait();  // the kernels before
   if (!kSlots) grid_launch_next();
   const int cap = max_blocks * B;
   const BlockDiv div(B);
@@ -420,24 +422,23 @@ cudaError_t launch_page_plan(const int32_t* have, const int32_t* want, const int
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
   }
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = 8;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cudaLaunchAttribute attr[2] = {};
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 8;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(one ? 1 : 8);
   cfg.blockDim = dim3(kPlanThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cfg.attrs = &attr;
-  cfg.numAttrs = one ? 0 : 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = one ? 1 : 2;
   const cudaError_t e =
       cudaLaunchKernelEx(&cfg, kernel, have, want, keep, batch, B, table, max_blocks, num_pages,
                          ring, pool, pool_out, got, cu, slots, max_new);
   if (e != cudaSuccess || one) return e;
-  attr = cudaLaunchAttribute{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.gridDim = dim3((unsigned)((max_new + 2047) / 2048));
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = 0;

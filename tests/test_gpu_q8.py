@@ -743,6 +743,55 @@ def test_plan_and_append_in_a_graph_and_on_another_stream(ssa):
             assert torch.equal(ref[0], o[0]) and torch.equal(ref[1], o[1])
 
 
+def test_steps_in_a_row_equal_steps_one_by_one(ssa):
+    """Every kernel starts while the one before it ends: 150 steps whose lengths, tables,
+    lists and queries change each time give the same without a wait between any two
+    calls as with one after each."""
+    B, d, Hkv, n, mb, cap = 16, 128, 2, 24, 40, 6000
+    r = np.random.default_rng(50)
+    pages = n * mb // 2
+    order = r.permutation(pages)
+    have, wants = np.zeros(n, np.int64), []
+    for i in range(150):
+        w = np.where(r.random(n) < 0.8, have + 1, have + r.integers(-300, 400, n))
+        wants.append(np.clip(w, 0, B * mb))
+        have = wants[-1]  # (some rows are refused: the plan takes what comes)
+    wants = [_dev(w) for w in wants]
+    g = torch.Generator(device=DEV).manual_seed(51)
+    k, v = (torch.randn(cap, Hkv, d, generator=g, device=DEV).bfloat16() for _ in range(2))
+    q = torch.randn(150, n, 8, d, generator=g, device=DEV).bfloat16()
+
+    def run(topk, wait):
+        K, V = (torch.zeros(pages, Hkv, B, d, dtype=torch.int8, device=DEV) for _ in range(2))
+        Ks, Vs = (torch.zeros(pages, Hkv, device=DEV) for _ in range(2))
+        S = torch.zeros(n, Hkv, mb, d, device=DEV)
+        lens = torch.zeros(n, dtype=torch.int32, device=DEV)
+        table = torch.full((n, mb), -1, dtype=torch.int32, device=DEV)
+        ring, pool = _dev(order), _dev(np.array([0, pages]))
+        q_in, outs = torch.empty_like(q[0]), []
+        for i, want in enumerate(wants):
+            q_in.copy_(q[i])
+            wait()
+            _, cu, slots, _ = ssa.ssa_page_plan(lens, want, table, ring, pool, B,
+                                                cap if i % 3 else 9000, got=lens, pool_out=pool)
+            wait()
+            kk, vv = (x if i % 3 else torch.cat([x, x[:3000]]) for x in (k, v))
+            ssa.ssa_append_paged_q8(K, Ks, V, Vs, S, slots, cu, lens, kk, vv, B)
+            wait()
+            outs.append(ssa.ssa_decode_paged_q8(q_in, K, Ks, V, Vs, S, table, lens, B, topk))
+            wait()
+        torch.cuda.synchronize()
+        return outs, (K, Ks, V, Vs, S, lens, table, ring, pool)
+
+    for topk in (3, 1 << 20):
+        ref = run(topk, torch.cuda.synchronize)
+        got = run(topk, lambda: None)
+        for a, b in zip(ref[1], got[1]):
+            assert torch.equal(a, b)
+        for (a, ia), (b, ib) in zip(ref[0], got[0]):
+            assert torch.equal(a, b) and torch.equal(ia, ib)
+
+
 @pytest.mark.parametrize("fmt,dtype", [("e4m3", "bf16"), ("i8", "f32")])
 def test_serving_steps_plan_append_decode(ssa, fmt, dtype):
     """Prompts, decode steps, a rollback, a finished and a refused request, as a
