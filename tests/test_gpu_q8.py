@@ -12,8 +12,8 @@ leaves 2^-22, and d / 16 accumulations each at most a step, 2^-23, of a partial
 sum no larger than A; with the products by scales below 2^-22.  So
 |dx| <= A (d / 16 + 4) 2^-23 =: e.  Probabilities then move by a factor within
 exp(2 e), P's split and ex2 by 2^-21, and the sums of at most 2^10 fp32 partial results by
-2^-20 of sum p |v| <= Vmax.  |dO| <= Vmax (2 e + 2^-19).  In bf16 half a step of the result,
-2^-8 |O|, comes on top.
+2^-20 of sum p |v| <= Vmax.  |dO| <= Vmax (2 e + 2^-19).  In bf16 P is one f16: half a step of
+each p, 2^-11, makes 2^-11 Vmax; and half a step of the result, 2^-8 |O|, comes on top.
 """
 import math
 
@@ -412,7 +412,7 @@ def _tolerance(q, K, Ks, Ls, scale, V, Vs, dtype, ref):
     e = A * (d / 16 + 4) * 2.0 ** -23
     vmax = np.abs(O.q8_values(np.nan_to_num(V), Vs)).max()
     tol = vmax * (2 * e + 2.0 ** -19)
-    return tol + (2.0 ** -8 * np.abs(ref) if dtype == "bf16" else 0.0)
+    return tol + (2.0 ** -11 * vmax + 2.0 ** -8 * np.abs(ref) if dtype == "bf16" else 0.0)
 
 
 def _run_decode(ssa, cache, q, L, B, topk, S=True, **kw):
