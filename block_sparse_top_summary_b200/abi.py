@@ -527,17 +527,27 @@ def _refuse(dev: int, *args):
             raise ValueError(f"{n} is on cuda:{t.get_device()}, the current device is cuda:{dev}")
 
 
-def _launch_on(stream, dev: int, own=()):
-    """The stream's handle; ``own``, tensors that the call has allocated, stay alive for
-    the work on a stream that is not the one they were allocated on."""
+def _launch_on(stream, dev: int):
+    """The stream's handle."""
     if stream is None:
         return _current_stream(dev)
     if stream.device_index != dev:
         raise ValueError(f"the stream is of cuda:{stream.device_index}, "
                          f"the current device is cuda:{dev}")
-    for t in own:
-        t.record_stream(stream)
     return stream.cuda_stream
+
+
+def _new(shape, dtype, like, stream):
+    """A tensor for the call to write on ``stream``.  It is allocated there (memory of the
+    current stream may still be in use by work before it) and, as the caller is going to
+    use it on the current stream, not given back before that one's work with it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    current = torch.cuda.current_stream()
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=like.device)
+    t.record_stream(current)
+    return t
 
 
 def ssa_page_plan(have, want, page_table, ring, pool, B: int, max_new: int, keep=None, got=None,
@@ -553,7 +563,7 @@ def ssa_page_plan(have, want, page_table, ring, pool, B: int, max_new: int, keep
     i32, dev = torch.int32, _device()
     batch, max_blocks = page_table.shape
     num_pages = ring.numel()
-    rows, two, own = (batch,), (2,), []
+    rows, two = (batch,), (2,)
     if (have.dtype is not i32 or have.shape != rows or want.dtype is not i32
             or want.shape != rows or page_table.dtype is not i32 or ring.dtype is not i32
             or ring.dim() != 1 or pool.dtype is not i32 or pool.shape != two
@@ -569,10 +579,11 @@ def ssa_page_plan(have, want, page_table, ring, pool, B: int, max_new: int, keep
     if got is not None or cu is not None or slots is not None or pool_out is not None:
         _refuse(dev, ("got", got, i32, rows), ("cu", cu, i32, (batch + 1,)),
                 ("slots", slots, i32, (max_new,)), ("pool_out", pool_out, i32, two))
+    handle = _launch_on(stream, dev)
     if got is None or cu is None or slots is None or pool_out is None:
         # the outputs that are not given, in one allocation
-        own.append(torch.empty(max_new + 2 * batch + 3, dtype=i32, device=have.device))
-        new = own[0].split_with_sizes((max_new, batch, batch + 1, 2))
+        new = _new((max_new + 2 * batch + 3,), i32, have, stream).split_with_sizes(
+            (max_new, batch, batch + 1, 2))
         slots = new[0] if slots is None else slots
         got = new[1] if got is None else got
         cu = new[2] if cu is None else cu
@@ -580,8 +591,7 @@ def ssa_page_plan(have, want, page_table, ring, pool, B: int, max_new: int, keep
     status = load_library().ssa_page_plan(
         have.data_ptr(), want.data_ptr(), None if keep is None else keep.data_ptr(), batch, B,
         page_table.data_ptr(), max_blocks, num_pages, ring.data_ptr(), pool.data_ptr(),
-        pool_out.data_ptr(), got.data_ptr(), cu.data_ptr(), slots.data_ptr(), max_new,
-        _launch_on(stream, dev, own))
+        pool_out.data_ptr(), got.data_ptr(), cu.data_ptr(), slots.data_ptr(), max_new, handle)
     _check("ssa_page_plan", status)
     return got, cu, slots, pool_out
 
@@ -682,15 +692,15 @@ def ssa_decode_paged_q8(q, Kp, Ks, Vp, Vs, S, page_table, seqlens, B: int, topk:
         _refuse(dev, ("q", q, q.dtype, (batch, Hq, d)),
                 ("page_table", page_table, i32, (batch, max_blocks)),
                 ("seqlens", seqlens, i32, (batch,)))
-    own = []
+    handle = _launch_on(stream, dev)
     if O is None:
-        own.append(O := torch.empty_like(q))
+        O = _new(heads, q.dtype, q, stream)
     else:
         _refuse(dev, ("O", O, q.dtype, heads))
     if idx is not None:
         _refuse(dev, ("idx", idx, i32, (batch, Hkv, width)))
     elif want_idx:
-        own.append(idx := torch.empty(batch, Hkv, width, dtype=i32, device=q.device))
+        idx = _new((batch, Hkv, width), i32, q, stream)
     at = ws_bytes = 0
     if workspace is not None:
         ws_bytes = workspace.numel()
@@ -698,14 +708,13 @@ def ssa_decode_paged_q8(q, Kp, Ks, Vp, Vs, S, page_table, seqlens, B: int, topk:
         at = workspace.data_ptr()
     elif (ws_bytes := ssa_decode_paged_q8_workspace_size(batch, Hq, Hkv, d, B, topk,
                                                          max_blocks)) > 0:
-        own.append(workspace := torch.empty(ws_bytes, dtype=torch.uint8, device=q.device))
+        workspace = _new((ws_bytes,), torch.uint8, q, stream)
         at = workspace.data_ptr()
     status = load_library().ssa_decode_paged_q8(
         q.data_ptr(), _dtype_code(q), Kp.data_ptr(), Ks.data_ptr(), Vp.data_ptr(), Vs.data_ptr(),
         fmt, None if S is None else S.data_ptr(), page_table.data_ptr(), max_blocks, num_pages,
         seqlens.data_ptr(), batch, Hq, Hkv, d, B, topk, d ** -0.5 if scale is None else scale,
-        O.data_ptr(), None if idx is None else idx.data_ptr(), at, ws_bytes,
-        _launch_on(stream, dev, own))
+        O.data_ptr(), None if idx is None else idx.data_ptr(), at, ws_bytes, handle)
     _check("ssa_decode_paged_q8", status)
     return O, idx
 

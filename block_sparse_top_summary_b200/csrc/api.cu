@@ -484,6 +484,9 @@ ssa_status ssa_decode_paged_q8(const void* q, ssa_dtype dtype, const void* Kp, c
   if ((long long)batch * max_blocks * (B / 16) > 0x7fffffffLL ||
       (long long)batch * Hkv > 0x7ffffffeLL)
     return SSA_ERR_UNSUPPORTED;
+  // and those of one of the split pass's blocks (148 at least) as well
+  const int kept = topk < max_blocks - 2 ? topk + 2 : max_blocks;
+  if ((long long)batch * Hkv * kept > (1LL << 37) / (B / 16)) return SSA_ERR_UNSUPPORTED;
   if (!(scale > 0.f)) return SSA_ERR_INVALID_ARG;
   if (q == nullptr || Kp == nullptr || Ks == nullptr || Vp == nullptr || Vs == nullptr ||
       page_table == nullptr || seqlens == nullptr || O == nullptr)

@@ -497,7 +497,7 @@ ssa_status ssa_append_paged_q8(void* Kp, float* Ks, void* Vp, float* Vs, ssa_qfo
  * values that the codes stand for.  q, O: [batch, Hq, d] of `dtype`.  Sums and
  * softmax are in fp32.  On the tensor cores, q and P in fp32 are sums of two f16
  * (22 bits, q relative to each head's largest coordinate); with bf16 P is one f16
- * (11 bits), and q is exact but for coordinates below 2^-12 of the head's
+ * (11 bits, and to 2^-29 of the largest p), and q is exact but for coordinates below 2^-12 of the head's
  * largest, which are held to 2^-20 of it.  The unnormalised sums of P times V
  * have to stay within fp32's range.
  *
@@ -506,10 +506,12 @@ ssa_status ssa_append_paged_q8(void* Kp, float* Ks, void* Vp, float* Vs, ssa_qfo
  * attention over the whole cache for every sequence.
  * seqlens, page_table, idx: as for ssa_decode_paged (a length outside
  * [1, max_blocks * B] writes zeros, and -1 to its idx rows).
+ * O and idx must not overlap the inputs.
  * workspace: >= ssa_decode_paged_q8_workspace_size(...) bytes, 256-byte aligned,
  * contents on entry ignored; calls that share one must not overlap on the
  * device.  The size is 0, and the workspace may be NULL, for a few short rows
- * read whole.  Hq / Hkv <= 8; max_blocks <= 16384.
+ * read whole.  Hq / Hkv <= 8; max_blocks <= 16384; batch * max_blocks * B / 16 < 2^31
+ * and batch * Hkv * (blocks attended by a row, at most) * B / 16 <= 2^37.
  */
 ssa_status ssa_decode_paged_q8_workspace_size(int batch, int Hq, int Hkv, int d, int B, int topk,
                                               int max_blocks, size_t* bytes);

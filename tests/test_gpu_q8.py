@@ -664,6 +664,34 @@ def test_decode_on_another_stream_in_a_graph_and_twice_at_once(ssa):
         assert torch.equal(outs[1][0], whole[i][0])
 
 
+def test_results_on_another_stream_leave_the_current_ones_memory_alone(ssa):
+    # memory freed behind a copy that the current stream has not run yet is not what a call
+    # on another stream writes its results to
+    B, d, n = 64, 128, 64
+    L = [100] * n
+    cache = _cache("e4m3", d, B, 2, L, seed=12)
+    K, Ks, V, Vs, S = (x.to(DEV) for x in cache[:5])
+    table, lens = _dev(cache[5]), _dev(np.asarray(L))
+    q = torch.randn(n, 16, d, device=DEV, dtype=torch.bfloat16)
+    have, want = _dev(np.zeros(n)), _dev(np.ones(n))
+    ring, pool = _dev(np.arange(2 * n)), _dev(np.array([0, 2 * n]))
+    ptable = torch.full((n, 4), -1, dtype=torch.int32, device=DEV)
+    ref = ssa.ssa_decode_paged_q8(q, K, Ks, V, Vs, S, table, lens, B, 4)
+    side = torch.cuda.Stream()
+    for i in range(3):
+        torch.cuda.synchronize()
+        held = [torch.full_like(q, 7.), torch.full_like(ref[1], 7), torch.full((n * 8,), 7, device=DEV)]
+        torch.cuda._sleep(20_000_000)  # cycles: some 10 ms
+        kept = [x.clone() for x in held]
+        del held
+        got = ssa.ssa_decode_paged_q8(q, K, Ks, V, Vs, S, table, lens, B, 4, stream=side)
+        plan = ssa.ssa_page_plan(have, want, ptable, ring, pool, B, 4 * n, stream=side)
+        torch.cuda.synchronize()
+        assert all((x == 7).all() for x in kept)
+        assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
+        assert plan[0].tolist() == [1] * n
+
+
 @pytest.mark.parametrize("G,d,topk", [(4, 128, 1 << 20), (1, 64, 1 << 20), (8, 128, 5)])
 def test_decode_repeats_bitwise(ssa, G, d, topk):
     # rows split between blocks: the block that joins a row's parts changes from run

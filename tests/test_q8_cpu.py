@@ -95,6 +95,10 @@ def test_decode_q8_rejections(lib):
     assert call(scale=0.0) == 1 and call(scale=float("nan")) == 1
     assert call(d=32) == 2 and call(B=24) == 2
     assert call(max_blocks=16385) == 2
+    # slices of the batch, and of the batch and its heads, past what the kernels count
+    assert call(max_blocks=16384, batch=40000) == 2
+    assert call(max_blocks=16384, batch=30000, Hq=4096, Hkv=4096, topk=1 << 30) == 2
+    assert call(max_blocks=16384, batch=30000, Hq=4096, Hkv=4096, topk=1 << 30, q=NULL) == 2
     n = ctypes.c_size_t(0)
     f = lib.ssa_decode_paged_q8_workspace_size
     assert f(2, 7, 2, 128, 64, 4, 64, ctypes.byref(n)) == 1
