@@ -69,6 +69,23 @@ __device__ __forceinline__ int pair_slices(int L, int B, int kk, int Lmax, int* 
   return (nb - 1) * (B / kSlice) + (tail + kSlice - 1) / kSlice;
 }
 
+// a / b for whole numbers that leave an int; in 32 bits where a fits (a 64-bit division is
+// a fifth of a microsecond).
+__device__ __forceinline__ int quotient(long long a, int b) {
+  return a >> 32 ? (int)(a / b) : (int)((uint32_t)a / (uint32_t)b);
+}
+
+// *p += v, as a release of what this thread knows written and an acquire of what others
+// have released there; the old value.  (__threadfence on both sides: 0.5 us more.)
+__device__ __forceinline__ int add_acq_rel(int* p, int v) {
+  int old;
+  asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], %2;"
+               : "=r"(old)
+               : "l"(p), "r"(v)
+               : "memory");
+  return old;
+}
+
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -414,8 +431,8 @@ __global__ void __launch_bounds__(kQThreads, 1) q8_split_kernel(
     const uint8_t* __restrict__ Vp, const float* __restrict__ Vs,
     const int32_t* __restrict__ table, const int32_t* __restrict__ seqlens, int batch, int Hq,
     int Hkv, int B, int max_blocks, int num_pages, int kk, int width, int lists, int whole_pairs,
-    int min_slices, int32_t* __restrict__ idx_out, const int32_t* __restrict__ ws_idx, const int32_t* __restrict__ ws_off,
-    float* __restrict__ ws_part, int* __restrict__ ws_ctr, T* __restrict__ O, float scale_log2) {
+    int32_t* __restrict__ idx_out, const int32_t* __restrict__ ws_idx,
+    const int32_t* __restrict__ ws_off, float* __restrict__ ws_part, int* __restrict__ ws_ctr, T* __restrict__ O, float scale_log2) {
   constexpr int TILE = kSlice * D;       // bytes of K (or V) of a slice
   constexpr int KS = D / 16;             // k steps of S
   constexpr int OT = D / 16;             // tiles of O^T
@@ -427,11 +444,11 @@ __global__ void __launch_bounds__(kQThreads, 1) q8_split_kernel(
   constexpr float kLazy = 8.0f, kUp = 4.0f, kNear = 8.0f;
   constexpr int stages = q8_stages(D);
   static_assert(stages * 2 * TILE >= REC * 4, "a warp's ring holds its record");
-  // sums that half of the last block's threads can exchange, [PS - 1][E] of 8 floats
-  constexpr int kJoinSums = kQW * REC / 2 > 2 * 8 * kQGridMax
-                                ? (kQW * REC / 2 - 2 * 8 * kQGridMax) / 8
-                                : 0;
-  static_assert(kQW * REC >= 2 * 2 * 8 * kQGridMax, "m and l of two pairs' records");
+  // the last block's room for two pairs: each m and l of all records, the threads' sums
+  // and kJoinStage float4 of records
+  constexpr int kJoinRoom = kQW * stages * 2 * TILE / 4;
+  constexpr int kJoinStage = (kJoinRoom / 2 - 16 * kQGridMax - 8 * kQThreads) / 4;
+  static_assert(kQThreads >= 8 * D / 4 && kJoinStage >= kQThreads, "PS and cap are 1 at least");
   // q against e4m3 codes, or in fp32: f16 against keys turned into f16, with a low part
   // in fp32.  q in bf16 against int8 codes: three int8 digits against the codes
   // themselves, which saves turning K (410 -> 392 instructions a slice; 32 ragged rows 116 -> 115 us, and under a sustained
@@ -446,7 +463,8 @@ __global__ void __launch_bounds__(kQThreads, 1) q8_split_kernel(
   __shared__ int s_pair[kQW][2];             // pair of a warp's first and last record, or -1
   __shared__ int s_list[2 * kQW];            // records in use
   __shared__ int s_from[kQW + 2], s_gpair[kQW + 1];  // a group's records in s_list, its pair
-  __shared__ int s_last[2];
+  __shared__ int s_split[2], s_first[2], s_parts[2];  // split pairs, their blocks
+  __shared__ int s_last[2];                           // those that this block joins
   __shared__ int32_t s_off[kQThreads + 1];
 
   const int G = Hq / Hkv, spb = B / kSlice;
@@ -477,9 +495,11 @@ __global__ void __launch_bounds__(kQThreads, 1) q8_split_kernel(
     grid_wait();
   }
   const long long total = (long long)off[batch] * Hkv;
-  // no more blocks than leave each some slices
-  const long long most = (total + min_slices - 1) / min_slices;
-  const long long grid = most < gridDim.x ? most : gridDim.x;
+  // no more blocks than leave each warp a slice; the first `extra` take run + 1 slices, the
+  // others run
+  const int grid = total < (long long)gridDim.x * kQW ? ((int)total + kQW - 1) / kQW
+                                                      : (int)gridDim.x;
+  int run = 0, extra = 0;
   long long s0, s1;
   if (whole_pairs) {
     // one pair a block, with what the route kernel does where there is one
@@ -500,12 +520,14 @@ __global__ void __launch_bounds__(kQThreads, 1) q8_split_kernel(
       return;
     }
   } else {
-    if (blockIdx.x >= grid) {  // also when there is nothing at all
+    if ((int)blockIdx.x >= grid) {  // also when there is nothing at all
       grid_wait();
       return;
     }
-    s0 = blockIdx.x * total / grid;
-    s1 = (blockIdx.x + 1) * total / grid;
+    run = quotient(total, grid);
+    extra = (int)(total - (long long)run * grid);
+    s0 = (long long)blockIdx.x * run + min((int)blockIdx.x, extra);
+    s1 = s0 + run + ((int)blockIdx.x < extra ? 1 : 0);
   }
   const int ns = (int)(s1 - s0);
   // the warp's run
@@ -915,6 +937,24 @@ __global__ void __launch_bounds__(kQThreads, 1) q8_split_kernel(
     return (long long)off[pb] * Hkv + (long long)(p - pb * Hkv) * (off[pb + 1] - off[pb]);
   };
   auto pair_len = [&](int p) { return off[p / Hkv + 1] - off[p / Hkv]; };
+  // Only the first and the last group can go on in other blocks.
+  const long long cut = (long long)extra * (run + 1);
+  auto block_of = [&](long long s) {
+    return s < cut ? quotient(s, run + 1) : extra + quotient(s - cut, run);
+  };
+  if (warp == kQW - 1 && lane < 2) {
+    const int p = groups > lane ? s_gpair[lane == 0 ? 0 : groups - 1] : -1;
+    bool split = false;
+    if (p >= 0 && !whole_pairs) {
+      const long long f = pair_first(p), e = f + pair_len(p);
+      split = f < s0 || e > s1;
+      if (split) {
+        s_first[lane] = block_of(f);
+        s_parts[lane] = block_of(e - 1) - s_first[lane] + 1;
+      }
+    }
+    s_split[lane] = split ? p : -1;
+  }
   const int E = G * (D / 4);  // float4 of a record
   for (int e = t; e < groups * E; e += kQThreads) {
     const int k = e / E, r = e - k * E;
@@ -955,87 +995,90 @@ __global__ void __launch_bounds__(kQThreads, 1) q8_split_kernel(
       }
     }
   }
-  // ---- pairs split between blocks: the last block to arrive joins the records.
-  // Only the block's first and last group can be such.
+  // ---- pairs split between blocks: the last block to arrive joins the records
   if (whole_pairs) return;
   grid_wait();  // the counters are 0 (nothing is left to wait for where lists were)
   __syncthreads();
-  auto block_of = [&](long long s) { return (int)(((s + 1) * grid + total - 1) / total - 1); };
   if (t < 2) {
-    s_last[t] = -1;
-    if (groups > t) {
-      const int p = s_gpair[t == 0 ? 0 : groups - 1];
-      const long long f = pair_first(p), e = f + pair_len(p);
-      if (f < s0 || e > s1) {
-        const int parts = block_of(e - 1) - block_of(f) + 1;
-        __threadfence();  // the records, which the barrier has put before this
-        if (atomicAdd(&ws_ctr[p], 1) == parts - 1) s_last[t] = p;
-        __threadfence();
-      }
-    }
+    const int p = s_split[t];
+    // (the barrier has put the records before this)
+    s_last[t] = p >= 0 && add_acq_rel(&ws_ctr[p], 1) == s_parts[t] - 1 ? p : -1;
   }
   __syncthreads();
-  // One pair for the whole block, or one for each half of it
+  // One pair for the whole block, or one for each half of it.  This runs once a launch,
+  // so its instructions come from L2: short loops, and the records by way of shared
+  // memory, cost less than many loads a thread in unrolled code.
   const bool two = s_last[0] >= 0 && s_last[1] >= 0;
   const int half = two && t >= kQThreads / 2 ? 1 : 0;
-  const int p = two ? s_last[half] : max(s_last[0], s_last[1]);
+  const int which = two ? half : s_last[0] >= 0 ? 0 : 1, p = s_last[which];
   if (p < 0) return;
   {
     const int nt = two ? kQThreads / 2 : kQThreads, tt = t - half * (kQThreads / 2);
-    const long long f = pair_first(p);
-    const int xf = block_of(f), parts = block_of(f + pair_len(p) - 1) - xf + 1;
+    const int xf = s_first[which], parts = s_parts[which];
     // the pair is the last of its first block and the first of the others
     auto record = [&](int x) { return ws_part + ((size_t)(xf + x) * 2 + (x == 0 ? 1 : 0)) * rec_g; };
-    // Threads e + E y take the records y, y + PS, ... of the float4 e, e + PS E, ...; m and l
-    // of all records and the threads' sums go through the warps' records' room.
-    float* room = rec0 + half * (kQW * REC / 2);
-    float2* ml = reinterpret_cast<float2*>(room);                  // [parts][8]
-    float* sums = room + 2 * 8 * kQGridMax;                        // [PS - 1][E][8]
-    // (PS, and so the order of the sums, does not depend on which pairs meet here)
-    const int PS = max(1, min(kQThreads / 2 / E, 1 + kJoinSums / E));
-    const int y = tt / E;
-    for (int i = tt; i < parts * G; i += nt) {
-      const float* r = record(i / G) + G * D + i % G;
-      ml[i / G * 8 + i % G] = make_float2(__ldcg(r), __ldcg(r + 8));
-    }
-    __syncthreads();
-    for (int e0 = 0; e0 < E; e0 += PS == 1 ? nt : E) {
-      const int e = PS == 1 ? e0 + tt : tt - y * E;
-      const bool in = PS == 1 ? e < E : y < PS;
-      const int h = e / (D / 4), d4 = (e - h * (D / 4)) * 4;
-      float num[4] = {0.f, 0.f, 0.f, 0.f}, den = 0.f;
-      if (in) {
+    // Sum e + E y: of the records y, y + PS, ... of float4 e.  (PS, and so the order of
+    // the sums, does not depend on which pairs meet here.)
+    const int PS = kQThreads / E, cap = kJoinStage / E / PS * PS;
+    float* ml = reinterpret_cast<float*>(q8_smem) + half * (kJoinRoom / 2);  // the rings are free
+    float* sums = ml + 16 * kQGridMax;                                       // [PS][E][8]
+    float4* stage = reinterpret_cast<float4*>(sums + 8 * kQThreads);         // [cap][E]
+    const uint32_t ml_s = (uint32_t)__cvta_generic_to_shared(ml);
+    const uint32_t stage_s = (uint32_t)__cvta_generic_to_shared(stage);
+    for (int i = tt; i < parts * 4; i += nt)
+      cp16(ml_s + i * 16, record(i >> 2) + G * D + (i & 3) * 4);
+    // (both halves make the same number of rounds, which have barriers)
+    const int most = two ? max(s_parts[0], s_parts[1]) : parts;
+    for (int x0 = 0; x0 < most; x0 += cap) {
+      const int n = min(cap, parts - x0);  // 0 or less: nothing is left for this half
+      for (int i = tt; i < n * E; i += nt) {
+        const int x = i / E;
+        cp16(stage_s + i * 16, record(x0 + x) + (i - x * E) * 4);
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      __syncthreads();
+      for (int it = tt; it < E * PS; it += nt) {
+        const int y = it / E, e = it - y * E, h = e / (D / 4);
         float M = -INFINITY;
-#pragma unroll 8
-        for (int x = 0; x < parts; ++x) M = fmaxf(M, ml[x * 8 + h].x);
 #pragma unroll 4
-        for (int x = PS == 1 ? 0 : y; x < parts; x += PS) {
-          const float4 o = __ldcg(reinterpret_cast<const float4*>(record(x) + h * D + d4));
-          const float2 w = ml[x * 8 + h];
-          const float a = w.x == -INFINITY ? 0.f : ex2(w.x - M);
-          num[0] = fmaf(a, o.x, num[0]);
-          num[1] = fmaf(a, o.y, num[1]);
-          num[2] = fmaf(a, o.z, num[2]);
-          num[3] = fmaf(a, o.w, num[3]);
-          den = fmaf(a, w.y, den);
+        for (int x = 0; x < parts; ++x) M = fmaxf(M, ml[x * 16 + h]);
+        float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
+        float den = 0.f;
+        float* sm = sums + it * 8;
+        if (x0 > 0) {
+          num = *reinterpret_cast<const float4*>(sm);
+          den = sm[4];
         }
-        if (PS > 1 && y > 0) {
-          float* sm = sums + ((y - 1) * E + e) * 8;
-          *reinterpret_cast<float4*>(sm) = make_float4(num[0], num[1], num[2], num[3]);
-          sm[4] = den;
+#pragma unroll 2
+        for (int x = y; x < n; x += PS) {
+          const float m = ml[(x0 + x) * 16 + h], a = m == -INFINITY ? 0.f : ex2(m - M);
+          const float4 o = stage[x * E + e];
+          num.x = fmaf(a, o.x, num.x);
+          num.y = fmaf(a, o.y, num.y);
+          num.z = fmaf(a, o.z, num.z);
+          num.w = fmaf(a, o.w, num.w);
+          den = fmaf(a, ml[(x0 + x) * 16 + 8 + h], den);
         }
+        *reinterpret_cast<float4*>(sm) = num;
+        sm[4] = den;
       }
       __syncthreads();
-      if (in && (PS == 1 || y == 0)) {
-        for (int z = 1; z < PS; ++z) {
-          const float* sm = sums + ((z - 1) * E + e) * 8;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) num[i] += sm[i];
-          den += sm[4];
-        }
-        store4(O + ((int64_t)(p / Hkv) * Hq + (p % Hkv) * G + h) * D + d4,
-               make_float4(num[0], num[1], num[2], num[3]), den == 0.f ? 0.f : 1.f / den);
+    }
+    for (int e = tt; e < E; e += nt) {
+      float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
+      float den = 0.f;
+#pragma unroll 1
+      for (int y = 0; y < PS; ++y) {
+        const float* sm = sums + (y * E + e) * 8;
+        const float4 v = *reinterpret_cast<const float4*>(sm);
+        num.x += v.x;
+        num.y += v.y;
+        num.z += v.z;
+        num.w += v.w;
+        den += sm[4];
       }
+      store4(O + ((int64_t)(p / Hkv) * Hq + (p % Hkv) * G) * D + e * 4, num,
+             den == 0.f ? 0.f : 1.f / den);
     }
   }
 }
@@ -1102,7 +1145,7 @@ static cudaError_t launch_q8_t(const Q8Plan& p, const void* q, const void* Kp, c
     return cudaLaunchKernelEx(&cfg, q8_split_kernel<T, D, F>, (const T*)q, (const uint8_t*)Kp, Ks,
                               (const uint8_t*)Vp, Vs, table, seqlens, batch, Hq, Hkv, B,
                               max_blocks, num_pages, p.kk, p.width, p.lists ? 1 : 0,
-                              whole ? 1 : 0, kQW, idx_out, (const int32_t*)ws_idx,
+                              whole ? 1 : 0, idx_out, (const int32_t*)ws_idx,
                               (const int32_t*)ws_off, ws_part, ws_ctr, (T*)O,
                               scale * 1.4426950408889634f);
   };
