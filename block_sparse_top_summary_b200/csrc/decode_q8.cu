@@ -239,7 +239,8 @@ __device__ __forceinline__ int rank_of(const uint32_t* keys, int u0, int step, i
 // candidates >= T, in index order, are few (about 110 of 1000 or 2000 for k <= 32),
 // and each counts those before it.  A list longer than kListCap (many equal scores)
 // is left to block_select_topk.  2046 candidates, k = 32: 2.8 us (4.4 us with the
-// k-th of 256 groups' maxima, found by ranking them, for T).
+// k-th of 256 groups' maxima, found by ranking them, for T); with the chosen placed by
+// rank and put in order among themselves, not by a scan over the list, 0.4 us less.
 // keys: 256 + kListCap words, list: kListCap entries of shared memory.
 __device__ int block_select_quick(const float* sc, int n, int k, int first, int32_t* out,
                                   uint32_t* keys, uint16_t* list, uint32_t* hist, int* sbuf) {
@@ -289,18 +290,26 @@ __device__ int block_select_quick(const float* sc, int n, int k, int first, int3
   }
   if (t < 4 && m + t < kListCap) lk[m + t] = 0;  // up to a multiple of 4
   __syncthreads();
-  // two threads a candidate, each against half of the list
-  int done = 0;
-  for (int i0 = 0; i0 < m; i0 += 128) {
-    const int i = i0 + (t >> 1);
+  // two threads a candidate, each against half of the list; the first k by rank
+  uint32_t* sel = keys;  // (the maxima have been read)
+  for (int i = t >> 1; i - (t >> 1) < m; i += 128) {
     const uint32_t key = i < m ? lk[i] : 0u;
     int r = i < m ? rank_of(lk, (t & 1) * 4, 8, m, key, i) : k;
     r += __shfl_xor_sync(0xffffffffu, r, 1);
-    const bool take = (t & 1) == 0 && r < k;
-    int tot;
-    const int at = block_excl_scan(take ? 1 : 0, sbuf, &tot);
-    if (take) out[done + at] = first + (int)list[i];
-    done += tot;
+    if ((t & 1) == 0 && r < k) sel[r] = list[i];
+  }
+  if (t < 4) sel[k + t] = 0xffffffffu;
+  __syncthreads();
+  // by index
+  if (t < k) {
+    const uint32_t v = sel[t];
+    int at = 0;
+#pragma unroll 4
+    for (int u = 0; u < k; u += 4) {
+      const uint4 x = *reinterpret_cast<const uint4*>(sel + u);
+      at += (x.x < v) + (x.y < v) + (x.z < v) + (x.w < v);
+    }
+    out[at] = first + (int)v;
   }
   return k;
 }
