@@ -537,15 +537,15 @@ def _launch_on(stream, dev: int):
     return stream.cuda_stream
 
 
-def _new(shape, dtype, like, stream):
-    """A tensor for the call to write on ``stream``.  It is allocated there (memory of the
+def _new(like, stream, *shape):
+    """A tensor of the type of ``like`` for the call to write on ``stream``.  It is allocated there (memory of the
     current stream may still be in use by work before it) and, as the caller is going to
     use it on the current stream, not given back before that one's work with it."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return like.new_empty(*shape)  # (a third of what torch.empty's arguments cost)
     current = torch.cuda.current_stream()
     with torch.cuda.stream(stream):
-        t = torch.empty(shape, dtype=dtype, device=like.device)
+        t = like.new_empty(*shape)
     t.record_stream(current)
     return t
 
@@ -567,22 +567,23 @@ def ssa_page_plan(have, want, page_table, ring, pool, B: int, max_new: int, keep
     if (have.dtype is not i32 or have.shape != rows or want.dtype is not i32
             or want.shape != rows or page_table.dtype is not i32 or ring.dtype is not i32
             or ring.dim() != 1 or pool.dtype is not i32 or pool.shape != two
+            or keep is not None and (keep.dtype is not i32 or keep.shape != rows
+                                     or keep.get_device() != dev or not keep.is_contiguous())
             or not (have.get_device() == want.get_device() == page_table.get_device()
                     == ring.get_device() == pool.get_device() == dev)
             or not (have.is_contiguous() and want.is_contiguous() and page_table.is_contiguous()
                     and ring.is_contiguous() and pool.is_contiguous())):
         _refuse(dev, ("have", have, i32, rows), ("want", want, i32, rows),
                 ("page_table", page_table, i32, (batch, max_blocks)),
-                ("ring", ring, i32, (num_pages,)), ("pool", pool, i32, two))
-    if keep is not None:
-        _refuse(dev, ("keep", keep, i32, rows))
+                ("ring", ring, i32, (num_pages,)), ("pool", pool, i32, two),
+                ("keep", keep, i32, rows))
     if got is not None or cu is not None or slots is not None or pool_out is not None:
         _refuse(dev, ("got", got, i32, rows), ("cu", cu, i32, (batch + 1,)),
                 ("slots", slots, i32, (max_new,)), ("pool_out", pool_out, i32, two))
     handle = _launch_on(stream, dev)
     if got is None or cu is None or slots is None or pool_out is None:
         # the outputs that are not given, in one allocation
-        new = _new((max_new + 2 * batch + 3,), i32, have, stream).split_with_sizes(
+        new = _new(have, stream, max_new + 2 * batch + 3).unsafe_split_with_sizes(
             (max_new, batch, batch + 1, 2))
         slots = new[0] if slots is None else slots
         got = new[1] if got is None else got
@@ -694,13 +695,13 @@ def ssa_decode_paged_q8(q, Kp, Ks, Vp, Vs, S, page_table, seqlens, B: int, topk:
                 ("seqlens", seqlens, i32, (batch,)))
     handle = _launch_on(stream, dev)
     if O is None:
-        O = _new(heads, q.dtype, q, stream)
+        O = _new(q, stream, *heads)
     else:
         _refuse(dev, ("O", O, q.dtype, heads))
     if idx is not None:
         _refuse(dev, ("idx", idx, i32, (batch, Hkv, width)))
     elif want_idx:
-        idx = _new((batch, Hkv, width), i32, q, stream)
+        idx = _new(seqlens, stream, batch, Hkv, width)
     at = ws_bytes = 0
     if workspace is not None:
         ws_bytes = workspace.numel()
@@ -708,7 +709,7 @@ def ssa_decode_paged_q8(q, Kp, Ks, Vp, Vs, S, page_table, seqlens, B: int, topk:
         at = workspace.data_ptr()
     elif (ws_bytes := ssa_decode_paged_q8_workspace_size(batch, Hq, Hkv, d, B, topk,
                                                          max_blocks)) > 0:
-        workspace = _new((ws_bytes,), torch.uint8, q, stream)
+        workspace = _new(Kp, stream, ws_bytes)  # (of one-byte elements)
         at = workspace.data_ptr()
     status = load_library().ssa_decode_paged_q8(
         q.data_ptr(), _dtype_code(q), Kp.data_ptr(), Ks.data_ptr(), Vp.data_ptr(), Vs.data_ptr(),
