@@ -538,11 +538,12 @@ def _launch_on(stream, dev: int):
 
 
 def _new(like, stream, *shape):
-    """A tensor of the type of ``like`` for the call to write on ``stream``.  It is allocated there (memory of the
-    current stream may still be in use by work before it) and, as the caller is going to
-    use it on the current stream, not given back before that one's work with it."""
+    """A tensor of the type of ``like`` for the call to write on ``stream``.  It is
+    allocated there (memory of the current stream may still be in use by work before it)
+    and, as the caller is going to use it on the current stream, not given back before
+    that one's work with it."""
     if stream is None:
-        return like.new_empty(*shape)  # (a third of what torch.empty's arguments cost)
+        return like.new_empty(*shape)  # 1.1 us (torch.empty with its keywords: 2.9 us)
     current = torch.cuda.current_stream()
     with torch.cuda.stream(stream):
         t = like.new_empty(*shape)

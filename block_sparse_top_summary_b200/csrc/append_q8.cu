@@ -13,10 +13,10 @@
 // has the next two heads' rows under way while it works on the present one's.  Units
 // of few rows (decode steps) are left to single warps, a head each, without a barrier.
 // 52233 tokens of 8 heads, d = 128, B = 64 (bf16 to e4m3; 0.32 GB): 229 us with one block of
-// 256 threads a tile and a bisection of dependent loads, 64 us (5.0 TB/s) this way, with
-// the arithmetic at 60% of the issue slots: 8 chunks a thread (4: 69 us) and
+// 256 threads a tile and a bisection of dependent loads, 62.5 us (5.2 TB/s) this way, with
+// the arithmetic at 57% of the issue slots: 8 chunks a thread (4: 69 us) and
 // mixed-precision FMAs on the bf16 elements (unpacked first: 76 us) cut that.  64 single
-// tokens: 17 us before, 4.4 us.
+// tokens: 17 us before, 3.6 us (calls back to back in a CUDA graph).
 //
 // Units of sequence b start at floor(cu[b] / B) + 2 b: n new tokens touch at most
 // floor(n / B) + 2 blocks, so the ranges do not meet, and a unit's sequence is found

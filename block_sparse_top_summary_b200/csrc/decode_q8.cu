@@ -18,12 +18,13 @@
 //      in shared memory, and a pair that is split between blocks is finished by the
 //      last of them, from the blocks' records in order.  The kernel starts while the
 //      route kernel runs (programmatic dependent launch) and waits only for lists.
-// Measured (B200, CUDA graph): 128K keys of 8 heads, d = 128, e4m3, read whole (0.27 GB):
-// 56 us, of which the stream takes 41 (6.5 TB/s), start, join and the last blocks' part
-// the rest; 32 ragged rows of up to 16K keys, int8 (0.67 GB): 115 us; 64 rows of 65536 keys,
-// top-32 (0.27 GB of summaries, 0.28 GB of codes): 110 us.  A first form with a barrier
-// of all warps at every pair's end, the heads as the tiles' rows and a serial join took 74,
-// 175 and 138 us.
+// Measured (B200, calls back to back in a CUDA graph): 128K keys of 8 heads, d = 128, e4m3,
+// read whole (0.27 GB): 53.4 us, of which the blocks' streams take 38 to 46 (24 of the 148 SMs
+// are a tenth slower under load), start and joins the rest; 32 ragged rows of up to 16K
+// keys, int8 (0.67 GB): 115 us (5.8 TB/s); 64 rows of 65536 keys, top-32 (0.27 GB of
+// summaries, 0.28 GB of codes): 104.6 us; one row of 128K keys, top-32: 17.9 us.  A first form
+// with a barrier of all warps at every pair's end, the heads as the tiles' rows and a
+// serial join took 74, 175, 138 and 39 us.
 //
 // Fragments.  m16n8k16 tiles, f16 in and fp32 out, with the cache as the row operand:
 // S^T = K q^T has a tile's 16 rows for the slice's keys and its 8 columns for the
@@ -441,7 +442,8 @@ __global__ void __launch_bounds__(kQThreads, 1) q8_split_kernel(
     const int32_t* __restrict__ table, const int32_t* __restrict__ seqlens, int batch, int Hq,
     int Hkv, int B, int max_blocks, int num_pages, int kk, int width, int lists, int whole_pairs,
     int32_t* __restrict__ idx_out, const int32_t* __restrict__ ws_idx,
-    const int32_t* __restrict__ ws_off, float* __restrict__ ws_part, int* __restrict__ ws_ctr, T* __restrict__ O, float scale_log2) {
+    const int32_t* __restrict__ ws_off, float* __restrict__ ws_part, int* __restrict__ ws_ctr,
+    T* __restrict__ O, float scale_log2) {
   constexpr int TILE = kSlice * D;       // bytes of K (or V) of a slice
   constexpr int KS = D / 16;             // k steps of S
   constexpr int OT = D / 16;             // tiles of O^T
@@ -460,11 +462,11 @@ __global__ void __launch_bounds__(kQThreads, 1) q8_split_kernel(
   static_assert(kQThreads >= 8 * D / 4 && kJoinStage >= kQThreads, "PS and cap are 1 at least");
   // q against e4m3 codes, or in fp32: f16 against keys turned into f16, with a low part
   // in fp32.  q in bf16 against int8 codes: three int8 digits against the codes
-  // themselves, which saves turning K (410 -> 392 instructions a slice; 32 ragged rows 116 -> 115 us, and under a sustained
-  // load, where int8 meets the power limit, 132 -> 127 us, with P in two f16).  e4m3 has no such
-  // tile: the one that PTX offers here turns its operands into f16 as well (9 to 12
-  // cycles an SM quarter for k = 32 at a latency of 47, f16 8.3 for k = 16 at 24), and
-  // was slower (56 -> 65 us for 128K keys).
+  // themselves, which saves turning K (with P in two f16, 410 -> 392 instructions a slice;
+  // 32 ragged rows under a sustained load, where int8 meets the power limit, 132 -> 127 us).
+  // e4m3 has no such tile: the one that PTX offers here turns its operands into f16 as
+  // well (9 to 12 cycles an SM quarter for k = 32 at a latency of 47, f16 8.3 for k = 16 at
+  // 24), and was slower (56 -> 65 us for 128K keys).
   constexpr bool kDigits = sizeof(T) == 2 && F == SSA_I8;
   constexpr bool kLow = sizeof(T) == 4;
   extern __shared__ __align__(128) unsigned char q8_smem[];
@@ -971,8 +973,8 @@ __global__ void __launch_bounds__(kQThreads, 1) q8_split_kernel(
     const int from = s_from[k], to = s_from[k + 1], p = s_gpair[k];
     auto at = [&](int x) {
       const int rc = s_list[x];
-      return rc & 1 ? reinterpret_cast<const float*>(q8_smem + (size_t)(rc >> 1) * stages * 2 * TILE)
-                    : rec0 + (rc >> 1) * REC;
+      const unsigned char* own = q8_smem + (size_t)(rc >> 1) * stages * 2 * TILE;
+      return rc & 1 ? reinterpret_cast<const float*>(own) : rec0 + (rc >> 1) * REC;
     };
     float M = -INFINITY;
 #pragma unroll 4
@@ -1025,7 +1027,9 @@ __global__ void __launch_bounds__(kQThreads, 1) q8_split_kernel(
     const int nt = two ? kQThreads / 2 : kQThreads, tt = t - half * (kQThreads / 2);
     const int xf = s_first[which], parts = s_parts[which];
     // the pair is the last of its first block and the first of the others
-    auto record = [&](int x) { return ws_part + ((size_t)(xf + x) * 2 + (x == 0 ? 1 : 0)) * rec_g; };
+    auto record = [&](int x) {
+      return ws_part + ((size_t)(xf + x) * 2 + (x == 0 ? 1 : 0)) * rec_g;
+    };
     // Sum e + E y: of the records y, y + PS, ... of float4 e.  (PS, and so the order of
     // the sums, does not depend on which pairs meet here.)
     const int PS = kQThreads / E, cap = kJoinStage / E / PS * PS;

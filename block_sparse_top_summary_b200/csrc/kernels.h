@@ -130,11 +130,12 @@ cudaError_t launch_append_q8(void* Kp, float* Ks, void* Vp, float* Vs, ssa_qform
                              int max_blocks, int num_pages, cudaStream_t st);
 
 struct Q8Plan {
-  int kk;     // effective top-k: min(topk, max_blocks)
-  int width;  // idx row width: kk + 2
+  int kk;      // effective top-k: min(topk, max_blocks)
+  int width;   // idx row width: kk + 2
   bool lists;  // whether a row can leave blocks out
   bool whole;  // whether a pair is one block's work
-  // scratch (none where whole and no lists): block lists (from 0), slices before each sequence, arrivals, partial records
+  // scratch (none where whole and no lists): block lists (from 0), slices before each
+  // sequence, arrivals, partial records
   size_t off_off, off_ctr, off_part, bytes;
 };
 Q8Plan plan_q8(int batch, int Hq, int Hkv, int d, int B, int topk, int max_blocks);

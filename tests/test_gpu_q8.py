@@ -662,6 +662,21 @@ def test_decode_on_another_stream_in_a_graph_and_twice_at_once(ssa):
         torch.cuda.synchronize()
         assert torch.equal(outs[0][0], want[i][0]) and torch.equal(outs[0][1], want[i][1])
         assert torch.equal(outs[1][0], whole[i][0])
+    # both streams' calls in one graph, side by side
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        outs = []
+        for q, s in zip(qs, streams):
+            s.wait_stream(torch.cuda.current_stream())
+            outs.append(call(q, stream=s))
+        for s in streams:
+            torch.cuda.current_stream().wait_stream(s)
+    for _ in range(3):
+        gr.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(outs, want):
+            assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+            a[0].zero_(), a[1].zero_()
 
 
 def test_results_on_another_stream_leave_the_current_ones_memory_alone(ssa):
