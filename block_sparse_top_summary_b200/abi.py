@@ -12,6 +12,7 @@ import ctypes
 import functools
 import math
 import os
+import struct
 
 import torch
 
@@ -34,7 +35,8 @@ EXPORTS = ("ssa_status_string", "ssa_version", "ssa_block_summary", "ssa_route",
            "ssa_route_entmax", "ssa_sparse_attn_fwd_prior", "ssa_route_hierarchical",
            "ssa_decode_per_head", "ssa_decode_per_head_workspace_size",
            "ssa_sparse_attn_bwd_workspace_size", "ssa_page_plan", "ssa_append_paged_q8",
-           "ssa_decode_paged_q8_workspace_size", "ssa_decode_paged_q8",
+           "ssa_decode_paged_q8_workspace_size", "ssa_decode_paged_q8", "ssa_page_plan_words",
+           "ssa_append_paged_q8_words", "ssa_decode_paged_q8_words",
            "ssa_device_error", "ssa_check_device_error", "ssa_debug_wait_timeout")
 
 
@@ -94,6 +96,8 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
     lib.ssa_decode_paged_q8_workspace_size.argtypes = [i, i, i, i, i, i, i, ctypes.POINTER(sz)]
     lib.ssa_decode_paged_q8.argtypes = [vp, i, vp, vp, vp, vp, i, vp, vp, i, i, vp, i, i, i, i, i,
                                         i, f, vp, vp, vp, sz, vp]
+    for name in ("ssa_page_plan", "ssa_append_paged_q8", "ssa_decode_paged_q8"):
+        getattr(lib, name + "_words").argtypes = [ctypes.c_char_p]
     for name in EXPORTS:
         if name not in ("ssa_status_string", "ssa_version"):
             getattr(lib, name).restype = i
@@ -505,10 +509,14 @@ def ssa_sparse_attn_bwd(Q, K, V, O, dO, lse, idx, cnt, B: int, scale: float | No
 # ------------------------------------------------- page plan and 8-bit paged cache
 # A serving step makes these calls back to back and their kernels take a few
 # microseconds, so the checks are one expression a call (spelt out by _refuse where it
-# fails), and the current device and stream are read without building torch's
-# Python objects for them.
+# fails), the current device and stream are read without building torch's
+# Python objects for them, and the arguments go in one packed array (24 ctypes
+# arguments cost 3 us, the array 0.8).
 _device = torch._C._cuda_getDevice
 _current_stream = torch._C._cuda_getCurrentRawStream
+_plan_words = struct.Struct("=16q").pack
+_append_words = struct.Struct("=22q").pack
+_decode_words = struct.Struct("=18qd5q").pack
 
 
 def _refuse(dev: int, *args):
@@ -590,10 +598,10 @@ def ssa_page_plan(have, want, page_table, ring, pool, B: int, max_new: int, keep
         got = new[1] if got is None else got
         cu = new[2] if cu is None else cu
         pool_out = new[3] if pool_out is None else pool_out
-    status = load_library().ssa_page_plan(
-        have.data_ptr(), want.data_ptr(), None if keep is None else keep.data_ptr(), batch, B,
+    status = load_library().ssa_page_plan_words(_plan_words(
+        have.data_ptr(), want.data_ptr(), 0 if keep is None else keep.data_ptr(), batch, B,
         page_table.data_ptr(), max_blocks, num_pages, ring.data_ptr(), pool.data_ptr(),
-        pool_out.data_ptr(), got.data_ptr(), cu.data_ptr(), slots.data_ptr(), max_new, handle)
+        pool_out.data_ptr(), got.data_ptr(), cu.data_ptr(), slots.data_ptr(), max_new, handle))
     _check("ssa_page_plan", status)
     return got, cu, slots, pool_out
 
@@ -653,11 +661,11 @@ def ssa_append_paged_q8(Kp, Ks, Vp, Vs, S, slots, cu, seqlens, k_new, v_new, B: 
             or v_new.stride() != strides or strides[2] != 1):
         raise ValueError(f"k_new and v_new must be {list(new)} on the current device (cuda:{dev}), "
                          "of one dtype, of equal strides and contiguous in d")
-    status = load_library().ssa_append_paged_q8(
+    status = load_library().ssa_append_paged_q8_words(_append_words(
         Kp.data_ptr(), Ks.data_ptr(), Vp.data_ptr(), Vs.data_ptr(), fmt,
-        None if S is None else S.data_ptr(), slots.data_ptr(), cu.data_ptr(), seqlens.data_ptr(),
+        0 if S is None else S.data_ptr(), slots.data_ptr(), cu.data_ptr(), seqlens.data_ptr(),
         k_new.data_ptr(), v_new.data_ptr(), _dtype_code(k_new), strides[0], strides[1], batch, T,
-        Hkv, d, B, max_blocks, num_pages, _launch_on(stream, dev))
+        Hkv, d, B, max_blocks, num_pages, _launch_on(stream, dev)))
     _check("ssa_append_paged_q8", status)
     return Kp, Ks, Vp, Vs, S
 
@@ -712,11 +720,11 @@ def ssa_decode_paged_q8(q, Kp, Ks, Vp, Vs, S, page_table, seqlens, B: int, topk:
                                                          max_blocks)) > 0:
         workspace = _new(Kp, stream, ws_bytes)  # (of one-byte elements)
         at = workspace.data_ptr()
-    status = load_library().ssa_decode_paged_q8(
+    status = load_library().ssa_decode_paged_q8_words(_decode_words(
         q.data_ptr(), _dtype_code(q), Kp.data_ptr(), Ks.data_ptr(), Vp.data_ptr(), Vs.data_ptr(),
-        fmt, None if S is None else S.data_ptr(), page_table.data_ptr(), max_blocks, num_pages,
+        fmt, 0 if S is None else S.data_ptr(), page_table.data_ptr(), max_blocks, num_pages,
         seqlens.data_ptr(), batch, Hq, Hkv, d, B, topk, d ** -0.5 if scale is None else scale,
-        O.data_ptr(), None if idx is None else idx.data_ptr(), at, ws_bytes, handle)
+        O.data_ptr(), 0 if idx is None else idx.data_ptr(), at, ws_bytes, handle))
     _check("ssa_decode_paged_q8", status)
     return O, idx
 

@@ -1,5 +1,6 @@
 // C ABI entry points: host-side argument checks, then the kernel launches.
 #include <cuda_runtime.h>
+#include <string.h>
 
 #include "kernels.h"
 #include "ssa.h"
@@ -32,6 +33,29 @@ ssa_status check_q8(int d, int B, ssa_qformat fmt, ssa_dtype dt, int Hkv, int ma
     return SSA_ERR_UNSUPPORTED;
   return SSA_OK;
 }
+
+// Arguments read in order from an array of 8-byte words.
+struct Words {
+  const char* at;
+  bool ok = true;  // every number fitted so far
+  explicit Words(const void* w) : at(static_cast<const char*>(w)) {}
+  template <typename T>
+  T next() {
+    T v;
+    memcpy(&v, at, sizeof(T));
+    at += 8;
+    return v;
+  }
+  int num() {
+    const long long v = next<long long>();
+    if (v != (int)v) ok = false;
+    return (int)v;
+  }
+  template <typename T>
+  T* ptr() {
+    return next<T*>();
+  }
+};
 
 ssa_status from_cuda(cudaError_t e) { return e == cudaSuccess ? SSA_OK : SSA_ERR_CUDA; }
 
@@ -503,6 +527,91 @@ ssa_status ssa_decode_paged_q8(const void* q, ssa_dtype dtype, const void* Kp, c
                                          max_blocks, num_pages, seqlens, batch, Hq, Hkv, d, B,
                                          scale, O, idx, workspace,
                                          reinterpret_cast<cudaStream_t>(stream)));
+}
+
+// (braces: the arguments are read from left to right)
+ssa_status ssa_page_plan_words(const void* words) {
+  if (words == nullptr) return SSA_ERR_INVALID_ARG;
+  Words w(words);
+  struct {
+    const int32_t *have, *want, *keep;
+    int batch, B;
+    int32_t* table;
+    int max_blocks, num_pages;
+    int32_t* ring;
+    const int32_t* pool;
+    int32_t *pool_out, *got, *cu, *slots;
+    int max_new;
+    CUstream_st* stream;
+  } a{w.ptr<const int32_t>(), w.ptr<const int32_t>(), w.ptr<const int32_t>(), w.num(), w.num(),
+      w.ptr<int32_t>(), w.num(), w.num(), w.ptr<int32_t>(), w.ptr<const int32_t>(),
+      w.ptr<int32_t>(), w.ptr<int32_t>(), w.ptr<int32_t>(), w.ptr<int32_t>(), w.num(),
+      w.ptr<CUstream_st>()};
+  if (!w.ok) return SSA_ERR_INVALID_ARG;
+  return ssa_page_plan(a.have, a.want, a.keep, a.batch, a.B, a.table, a.max_blocks, a.num_pages,
+                       a.ring, a.pool, a.pool_out, a.got, a.cu, a.slots, a.max_new, a.stream);
+}
+
+ssa_status ssa_append_paged_q8_words(const void* words) {
+  if (words == nullptr) return SSA_ERR_INVALID_ARG;
+  Words w(words);
+  struct {
+    void* Kp;
+    float* Ks;
+    void* Vp;
+    float* Vs;
+    int fmt;
+    float* S;
+    const int32_t *slots, *cu, *seqlens;
+    const void *k_new, *v_new;
+    int dtype;
+    long long tok_stride, head_stride;
+    int batch, max_new, Hkv, d, B, max_blocks, num_pages;
+    CUstream_st* stream;
+  } a{w.ptr<void>(), w.ptr<float>(), w.ptr<void>(), w.ptr<float>(), w.num(), w.ptr<float>(),
+      w.ptr<const int32_t>(), w.ptr<const int32_t>(), w.ptr<const int32_t>(),
+      w.ptr<const void>(), w.ptr<const void>(), w.num(), w.next<long long>(),
+      w.next<long long>(), w.num(), w.num(), w.num(), w.num(), w.num(), w.num(), w.num(),
+      w.ptr<CUstream_st>()};
+  if (!w.ok) return SSA_ERR_INVALID_ARG;
+  return ssa_append_paged_q8(a.Kp, a.Ks, a.Vp, a.Vs, (ssa_qformat)a.fmt, a.S, a.slots, a.cu,
+                             a.seqlens, a.k_new, a.v_new, (ssa_dtype)a.dtype, a.tok_stride,
+                             a.head_stride, a.batch, a.max_new, a.Hkv, a.d, a.B, a.max_blocks,
+                             a.num_pages, a.stream);
+}
+
+ssa_status ssa_decode_paged_q8_words(const void* words) {
+  if (words == nullptr) return SSA_ERR_INVALID_ARG;
+  Words w(words);
+  struct {
+    const void* q;
+    int dtype;
+    const void* Kp;
+    const float* Ks;
+    const void* Vp;
+    const float* Vs;
+    int fmt;
+    const float* S;
+    const int32_t* table;
+    int max_blocks, num_pages;
+    const int32_t* seqlens;
+    int batch, Hq, Hkv, d, B, topk;
+    double scale;
+    void* O;
+    int32_t* idx;
+    void* workspace;
+    long long ws_bytes;
+    CUstream_st* stream;
+  } a{w.ptr<const void>(), w.num(), w.ptr<const void>(), w.ptr<const float>(),
+      w.ptr<const void>(), w.ptr<const float>(), w.num(), w.ptr<const float>(),
+      w.ptr<const int32_t>(), w.num(), w.num(), w.ptr<const int32_t>(), w.num(), w.num(),
+      w.num(), w.num(), w.num(), w.num(), w.next<double>(), w.ptr<void>(), w.ptr<int32_t>(),
+      w.ptr<void>(), w.next<long long>(), w.ptr<CUstream_st>()};
+  if (!w.ok || a.ws_bytes < 0) return SSA_ERR_INVALID_ARG;
+  return ssa_decode_paged_q8(a.q, (ssa_dtype)a.dtype, a.Kp, a.Ks, a.Vp, a.Vs, (ssa_qformat)a.fmt,
+                             a.S, a.table, a.max_blocks, a.num_pages, a.seqlens, a.batch, a.Hq,
+                             a.Hkv, a.d, a.B, a.topk, (float)a.scale, a.O, a.idx, a.workspace,
+                             (size_t)a.ws_bytes, a.stream);
 }
 
 ssa_status ssa_device_error(int* code) {

@@ -70,7 +70,7 @@ const char* ssa_status_string(int status);
  * ssa_decode_per_head, ssa_decode_per_head_workspace_size); 2.04 the backward
  * takes a sized workspace (ssa_sparse_attn_bwd_workspace_size) in place of
  * its delta scratch; 2.05 the page plan (ssa_page_plan) and the 8-bit paged
- * cache (ssa_append_paged_q8, ssa_decode_paged_q8). */
+ * cache (ssa_append_paged_q8, ssa_decode_paged_q8), and their packed forms. */
 int ssa_version(void);
 
 /*
@@ -522,6 +522,16 @@ ssa_status ssa_decode_paged_q8(const void* q, ssa_dtype dtype, const void* Kp, c
                                const int32_t* seqlens, int batch, int Hq, int Hkv, int d, int B,
                                int topk, float scale, void* O, int32_t* idx, void* workspace,
                                size_t ws_bytes, ssa_stream stream);
+
+/*
+ * The three calls above with their arguments in one array of 8-byte words, in order:
+ * pointers and whole numbers as signed 64-bit words, scale as a double.  For
+ * bindings whose calls cost by the argument.  A number that does not fit its
+ * argument's type is SSA_ERR_INVALID_ARG.
+ */
+ssa_status ssa_page_plan_words(const void* words);       /* 16 */
+ssa_status ssa_append_paged_q8_words(const void* words); /* 22 */
+ssa_status ssa_decode_paged_q8_words(const void* words); /* 24 */
 
 /*
  * Largest scratch area ssa_decode_noalloc can use (40 MiB).

@@ -111,6 +111,41 @@ def test_decode_q8_rejections(lib):
     assert abi.ssa_decode_paged_q8_workspace_size(64, 32, 8, 128, 64, 1 << 30, 16384) < 16 << 20
 
 
+def test_words_are_the_calls_arguments(lib):
+    """The packed forms refuse and accept what the calls do, word by word."""
+    fake = FAKE.value
+    plan = [fake] * 3 + [4, 64, fake, 8, 40] + [fake] * 6 + [10, 0]
+    append = [fake] * 4 + [0] + [fake] * 6 + [1, 256, 128, 2, 10, 2, 128, 64, 8, 40, 0]
+    need = abi.ssa_decode_paged_q8_workspace_size(2, 8, 2, 128, 64, 4, 64)
+    decode = [fake, 1] + [fake] * 4 + [0, fake, fake, 64, 200, fake, 2, 8, 2, 128, 64, 4, 0.088,
+                                       fake, 0, fake, need, 0]
+    assert lib.ssa_page_plan_words(None) == 1
+    # one argument at a time: what each call answers to a null pointer, an odd one, a number
+    # out of its range or its type's
+    for name, pack, ok in (("ssa_page_plan", abi._plan_words, plan),
+                           ("ssa_append_paged_q8", abi._append_words, append),
+                           ("ssa_decode_paged_q8", abi._decode_words, decode)):
+        words, call = getattr(lib, name + "_words"), getattr(lib, name)
+        for i, v in enumerate(ok):
+            bad = ([-1.0] if isinstance(v, float) else [0, fake + 2] if v == fake
+                   else [0] if v == need else [-5])
+            for x in bad:
+                a = ok[:i] + [x] + ok[i + 1:]
+                if i == len(ok) - 1 or (name, i) in OPTIONAL and x == 0:
+                    continue  # (these would launch)
+                want = call(*a)
+                assert want in (1, 2), (name, i, x)
+                assert words(pack(*a)) == want, (name, i, x)
+            if 0 < v < fake and not isinstance(v, float) and (name, i) not in WIDE:
+                a = ok[:i] + [v + (1 << 32)] + ok[i + 1:]
+                assert words(pack(*a)) == 1, (name, i)
+
+
+# arguments that may be null, and those of 64 bits
+OPTIONAL = {("ssa_page_plan", 2), ("ssa_append_paged_q8", 5), ("ssa_decode_paged_q8", 20)}
+WIDE = {("ssa_append_paged_q8", 12), ("ssa_append_paged_q8", 13), ("ssa_decode_paged_q8", 22)}
+
+
 def test_binding_refuses_what_is_not_on_a_gpu(monkeypatch):
     monkeypatch.setattr(abi, "_device", lambda: 0)
     K, s = torch.zeros(4, 2, 16, 64, dtype=torch.int8), torch.zeros(4, 2)
