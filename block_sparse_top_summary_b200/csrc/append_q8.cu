@@ -207,21 +207,30 @@ __global__ void __launch_bounds__(512) append_q8_kernel(
     const bool grown = r0 > 0 && !nan && scale > old;
     if (grown || (mean && r0 > 0)) {
       const float ratio = grown ? old * inv : 1.f;
-#pragma unroll 4
-      for (int r = rr; r < r0; r += rps) {
-        float y[8];
-        uint2 c = *reinterpret_cast<const uint2*>(P + r * D);
-        if (grown) {
-          q8_unpack8<F>(c, y);
+      for (int q = rr; q < r0; q += kChunks * rps) {
+        uint2 held[kChunks];  // read together, ahead of the first write
 #pragma unroll
-          for (int e = 0; e < 8; ++e) y[e] *= ratio;
-          c = q8_pack8<F>(y);
-          *reinterpret_cast<uint2*>(P + r * D) = c;
-        }
-        if (mean) {
-          q8_unpack8<F>(c, y);
+        for (int i = 0; i < kChunks; ++i)
+          if (q + i * rps < r0) held[i] = *reinterpret_cast<const uint2*>(P + (q + i * rps) * D);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) sum[e] += y[e];
+        for (int i = 0; i < kChunks; ++i) {
+          const int r = q + i * rps;
+          if (r < r0) {
+            float y[8];
+            uint2 c = held[i];
+            if (grown) {
+              q8_unpack8<F>(c, y);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) y[e] *= ratio;
+              c = q8_pack8<F>(y);
+              *reinterpret_cast<uint2*>(P + r * D) = c;
+            }
+            if (mean) {
+              q8_unpack8<F>(c, y);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) sum[e] += y[e];
+            }
+          }
         }
       }
     }
