@@ -13,8 +13,8 @@
 // has the next two heads' rows under way while it works on the present one's.  Units
 // of few rows (decode steps) are left to single warps, a head each, without a barrier.
 // 52233 tokens of 8 heads, d = 128, B = 64 (bf16 to e4m3; 0.32 GB): 229 us with one block of
-// 256 threads a tile and a bisection of dependent loads, 57 us (5.7 TB/s) this way, with
-// the arithmetic at some 60% of the issue slots: 8 chunks a thread (4: 69 us) and
+// 256 threads a tile and a bisection of dependent loads, 54 us (6.0 TB/s) this way, with
+// the arithmetic at some 65% of the issue slots: 8 chunks a thread (4: 69 us) and
 // mixed-precision FMAs on the bf16 elements (unpacked first: 76 us) cut that.  64 single
 // tokens: 17 us before, 3.6 us (calls back to back in a CUDA graph).
 //
@@ -208,7 +208,8 @@ __global__ void __launch_bounds__(512) append_q8_kernel(
     if (grown || (mean && r0 > 0)) {
       const float ratio = grown ? old * inv : 1.f;
       for (int q = rr; q < r0; q += kChunks * rps) {
-        uint2 held[kChunks];  // read together, ahead of the first write
+        // read together, ahead of the first write (each on its own: 64 us for the 52 K tokens)
+        uint2 held[kChunks];
 #pragma unroll
         for (int i = 0; i < kChunks; ++i)
           if (q + i * rps < r0) held[i] = *reinterpret_cast<const uint2*>(P + (q + i * rps) * D);
@@ -341,14 +342,13 @@ static cudaError_t launch_append_q8_t(void* Kp, float* Ks, void* Vp, float* Vs, 
   // each of 148 SMs), else fewer.
   int heads = Hkv;
   while (heads > 1 && units * 2 * ((Hkv + heads - 1) / heads) < 2 * 148) heads = (heads + 1) / 2;
-  // Up to four waves of blocks of all heads (512 threads an SM at 128 registers), half of the
-  // heads a block, but 4 at least: blocks whose page held rows before take longer, and
-  // the last wave's idle SMs cost more than a second start of the pipeline.  All heads and
-  // half of 8 (bf16, d = 128, B = 64), us: ragged prompts of 20 K tokens 41, 32; of 52 K 63, 57;
-  // of 65 K 73, 69; of 106 K 103, 107; 53 K in equal sequences 53.9, 55.3.  (Two heads of
-  // four: 36.4, 38.9.)
+  // Up to one and a half waves of blocks of all heads (512 threads an SM at 128 registers),
+  // half of the heads a block, but 4 at least: the last wave's idle SMs cost more than a
+  // second start of the pipeline.  All heads and half of 8 (bf16, d = 128, B = 64; 16 ragged
+  // prompts), us: 12 K tokens 19.0, 15.7; 20 K 28.9, 25.9; 33 K 35.6, 36.6; 52 K 53.4, 54.8.
+  // (Two heads of four: 65 K tokens 36.4, 38.9.)
   const long long blocks = 2 * (T_max / B + (long long)batch);
-  if (heads == Hkv && Hkv >= 7 && blocks * threads < 4LL * 148 * 512) heads = (Hkv + 1) / 2;
+  if (heads == Hkv && Hkv >= 7 && 2 * blocks * threads < 3LL * 148 * 512) heads = (Hkv + 1) / 2;
   const dim3 grid((unsigned)units, (unsigned)(2 * ((Hkv + heads - 1) / heads)));
   // two heads' rows (16 KB each for 64 rows of 128 in bf16), and the threads' sums
   const int smem = threads * (2 * chunks * 8 * (int)sizeof(T) + 8 * (int)sizeof(float));
