@@ -30,14 +30,14 @@
 // S^T = K q^T has a tile's 16 rows for the slice's keys and its 8 columns for the
 // group's heads, O^T = V^T P^T its rows for 16 coordinates.  So no row is idle (with
 // the heads as rows half of them are), and the f16 pairs of a code word are its
-// operands as they come.  In fp32 q and P are held as the sum of two f16, 22 bits: two
-// products with one row operand and one accumulator.  In bf16 q is exact in one f16,
-// and P is rounded to one: off by 2^-11 of each p, an eighth of a step of the bf16 result,
-// for a third of the tensor work (32 ragged rows, int8, under a sustained load 127 -> 113
-// us).  A thread reads 16 bytes of a key row at a time: the order of the coordinates
-// within a product is free, as long as q has the same.  The order of the keys is
-// pi(row), chosen with the chunk swizzle so that neither K nor V reads have bank
-// conflicts.  P^T is the S^T tile transposed (movmatrix).
+// operands as they come.  P is held as the sum of two f16, 22 bits, and so is q in fp32: two
+// products with one row operand and one accumulator.  q in bf16 is exact in one f16.  (P
+// in one f16, 11 bits, would take a third off the tensor work, 32 ragged rows of int8 under a
+// sustained load 127 -> 113 us, but an eighth of a step of the bf16 result shows in one result
+// in ten and, where the values cancel, in far more than a step.)  A thread reads 16 bytes of
+// a key row at a time: the order of the coordinates within a product is free, as long as
+// q has the same.  The order of the keys is pi(row), chosen with the chunk swizzle so that
+// neither K nor V reads have bank conflicts.  P^T is the S^T tile transposed (movmatrix).
 #include "common.cuh"
 #include "kernels.h"
 #include "q8.cuh"
@@ -839,7 +839,7 @@ __global__ void __launch_bounds__(kQThreads, 1) q8_split_kernel(
           }
         }
         // p is raised by 2^kUp, which l has too: more of P is in f16's normal range
-        uint32_t hi[2], lo[kLow ? 2 : 1];
+        uint32_t hi[2], lo[2];
         {
           const float m0 = (m_run[0] == -INFINITY ? 0.f : m_run[0]) - kUp;
           const float m1 = (m_run[1] == -INFINITY ? 0.f : m_run[1]) - kUp;
@@ -848,13 +848,9 @@ __global__ void __launch_bounds__(kQThreads, 1) q8_split_kernel(
             const float p0 = ex2(x[y][0] - m0), p1 = ex2(x[y][1] - m1);
             l_run[0] += p0;
             l_run[1] += p1;
-            if constexpr (kLow) {
-              split_half2(p0 * ratio, p1 * ratio, hi[y], lo[y]);
-              lo[y] = transpose8(lo[y]);
-            } else {
-              hi[y] = half2_bits(p0 * ratio, p1 * ratio);
-            }
+            split_half2(p0 * ratio, p1 * ratio, hi[y], lo[y]);
             hi[y] = transpose8(hi[y]);
+            lo[y] = transpose8(lo[y]);
           }
         }
         // O^T += V^T P^T
@@ -868,7 +864,7 @@ __global__ void __launch_bounds__(kQThreads, 1) q8_split_kernel(
             q8_to_half4<F>(__byte_perm(r[0][w], r[1][w], sel), a0, a1);
             q8_to_half4<F>(__byte_perm(r[2][w], r[3][w], sel), a2, a3);
             mma16(oc[2 * w + h], a0, a1, a2, a3, hi[0], hi[1]);
-            if constexpr (kLow) mma16(oc[2 * w + h], a0, a1, a2, a3, lo[0], lo[kLow ? 1 : 0]);
+            mma16(oc[2 * w + h], a0, a1, a2, a3, lo[0], lo[1]);
           }
       }
       st = st == stages - 1 ? 0 : st + 1;
