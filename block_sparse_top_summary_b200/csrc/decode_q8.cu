@@ -450,9 +450,12 @@ __global__ void __launch_bounds__(kQThreads, 1) q8_split_kernel(
   constexpr int CPR = D / 16;            // 16-byte chunks of a row
   constexpr int NCP = kSlice * CPR / 32; // chunks a lane copies
   constexpr int REC = 8 * (D + 2);       // floats of a warp's record
-  // P stays below 2^(kLazy + kUp + 3) = 2^15, within f16: O is rescaled when the
-  // maximum grows by more than kLazy (log2), or V's scale leaves [vref / 8, 8 vref]
-  constexpr float kLazy = 8.0f, kUp = 4.0f, kNear = 8.0f;
+  // P is p vs f in f16, vs the scale of V and f a power of two of each head that has the
+  // largest weight p vs met so far at 2^kUp or below 2^(kUp + 1).  m (log2) and f change when p
+  // passes 2^kLazy or vs f passes kMost, so P stays within 2^15.
+  constexpr float kLazy = 8.0f, kMost = 128.0f;
+  constexpr int kUp = 4;
+  static_assert(kMost * 256.0f <= 32768.0f, "kMost 2^kLazy is within f16");
   constexpr int stages = q8_stages(D);
   static_assert(stages * 2 * TILE >= REC * 4, "a warp's ring holds its record");
   // the last block's room for two pairs: each m and l of all records, the threads' sums
@@ -716,8 +719,8 @@ __global__ void __launch_bounds__(kQThreads, 1) q8_split_kernel(
       }
     }
     float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
-    // O is kept in units of vref, a scale of V met so far
-    float vref = 1.f, vinv = 1.f;
+    // O is kept times f; w: the largest weight so far, with m the reference of its p
+    float f[2] = {1.f, 1.f}, w[2] = {0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < OT; ++i) oc[i][0] = oc[i][1] = oc[i][2] = oc[i][3] = 0.f;
 
@@ -793,62 +796,43 @@ __global__ void __launch_bounds__(kQThreads, 1) q8_split_kernel(
           for (int y = 0; y < 2; ++y)
             if (ka + 8 * y >= rows) x[y][0] = x[y][1] = -INFINITY;
         }
-        const float c0 = fmaxf(x[0][0], x[1][0]), c1 = fmaxf(x[0][1], x[1][1]);
-        if (__any_sync(0xffffffffu, c0 > m_run[0] + kLazy || c1 > m_run[1] + kLazy)) {
+        const float c0 = fmaxf(x[0][0], x[1][0]), c1 = fmaxf(x[0][1], x[1][1]), vs = mi.z;
+        if (__any_sync(0xffffffffu, c0 > m_run[0] + kLazy || c1 > m_run[1] + kLazy ||
+                                        vs * f[0] > kMost || vs * f[1] > kMost)) {
           float cm[2] = {c0, c1};
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1)
               cm[e] = fmaxf(cm[e], __shfl_xor_sync(0xffffffffu, cm[e], o));
-            cm[e] = fmaxf(cm[e], m_run[e]);
-            const float alpha = m_run[e] == cm[e] ? 1.f : ex2(m_run[e] - cm[e]);  // 0 at first
+            const float m = fmaxf(cm[e], m_run[e]);
+            const float alpha = m_run[e] == m ? 1.f : ex2(m_run[e] - m);  // 0 at first
+            // (a NaN is no maximum: it marks p, not w)
+            w[e] = fmaxf(w[e] * alpha, cm[e] == -INFINITY ? 0.f : ex2(cm[e] - m) * vs);
+            // f = 2^kUp over w's power of two, within 2^126, so that 1 / f is exact
+            const int fe = min(254 + kUp - (int)(__float_as_uint(w[e]) >> 23), 253);
+            const float fn = __uint_as_float((uint32_t)fe << 23);
+            const float by = alpha * fn * __uint_as_float(0x7f000000u - __float_as_uint(f[e]));
             l_run[e] *= alpha;
+            f[e] = fn;
 #pragma unroll
-            for (int i = 0; i < OT; ++i) {
-              oc[i][e] *= alpha;
-              oc[i][e + 2] *= alpha;
+            for (int i = 0; i < OT; ++i) {  // (by <= 2: w has not fallen below alpha times itself)
+              oc[i][e] *= by;
+              oc[i][e + 2] *= by;
             }
-            m_run[e] = cm[e];
+            m_run[e] = m;
           }
         }
-        // P times the scale of V, as a factor of vref near 1
-        const float vs = mi.z;
-        float ratio = vs * vinv;
-        if (!(ratio <= kNear && ratio >= 1.f / kNear) && vs != 0.f) {
-          const float inv = 1.f / fmaxf(vs, 1.17549435e-38f);
-          const float by = vref * inv;  // O in units of vs
-          bool any = false;
-#pragma unroll
-          for (int i = 0; i < OT; ++i)
-            any |= oc[i][0] != 0.f || oc[i][1] != 0.f || oc[i][2] != 0.f || oc[i][3] != 0.f;
-          any = __any_sync(0xffffffffu, any);
-          // an O over 2^60 times what this block can add stays as it is
-          if (!(any && by > 1.152921504606847e18f)) {
-            const float f = any ? by : 0.f;
-#pragma unroll
-            for (int i = 0; i < OT; ++i) {
-              oc[i][0] *= f;
-              oc[i][1] *= f;
-              oc[i][2] *= f;
-              oc[i][3] *= f;
-            }
-            vref = vs;
-            vinv = inv;
-            ratio = vs * inv;
-          }
-        }
-        // p is raised by 2^kUp, which l has too: more of P is in f16's normal range
         uint32_t hi[2], lo[2];
         {
-          const float m0 = (m_run[0] == -INFINITY ? 0.f : m_run[0]) - kUp;
-          const float m1 = (m_run[1] == -INFINITY ? 0.f : m_run[1]) - kUp;
+          const float m0 = m_run[0] == -INFINITY ? 0.f : m_run[0];
+          const float m1 = m_run[1] == -INFINITY ? 0.f : m_run[1];
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
             const float p0 = ex2(x[y][0] - m0), p1 = ex2(x[y][1] - m1);
             l_run[0] += p0;
             l_run[1] += p1;
-            split_half2(p0 * ratio, p1 * ratio, hi[y], lo[y]);
+            split_half2(p0 * vs * f[0], p1 * vs * f[1], hi[y], lo[y]);
             hi[y] = transpose8(hi[y]);
             lo[y] = transpose8(lo[y]);
           }
@@ -877,9 +861,14 @@ __global__ void __launch_bounds__(kQThreads, 1) q8_split_kernel(
 #pragma unroll
       for (int o = 4; o < 32; o <<= 1) l_run[e] += __shfl_xor_sync(0xffffffffu, l_run[e], o);
 #pragma unroll
-    for (int i = 0; i < OT; ++i)
+    for (int e = 0; e < 2; ++e) {
+      const float by = __uint_as_float(0x7f000000u - __float_as_uint(f[e]));  // 1 / f
 #pragma unroll
-      for (int e = 0; e < 4; ++e) oc[i][e] *= vref;
+      for (int i = 0; i < OT; ++i) {
+        oc[i][e] *= by;
+        oc[i][e + 2] *= by;
+      }
+    }
     const int pair = b * Hkv + g;
     if (begins && ends) {
       // nobody else has a part of it; no key at all gives zeros

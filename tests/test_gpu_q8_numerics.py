@@ -10,7 +10,10 @@ With p_t = exp(x_t - max x), l = sum p, and a row's largest weight W = max_t p_t
   runs (up to 2^4 slices of 16 keys a warp) and their joins less than 2^-20, all of sum p |v| / l;
   2^-19 in all;
 - a p below the f16 parts' last bit is off by half of it;
-- a bf16 result is rounded by half a step, 2^-8 of itself at most.
+- a p below 2^-126 is 0 in fp32 (ex2 flushes it; p refers to a maximum not above the row's, so
+  no larger p is): what such keys add may be missing, the sum of their p |v| / l;
+- a bf16 result is rounded by half a step, 2^-8 of itself at most, or 2^-134 where it is
+  subnormal.
 
 P's last bit: ``FLOOR`` of W for each key, the keys being those that a warp holds together.
 """
@@ -36,12 +39,13 @@ def ssa():
 
 
 def _reference(q, K, Ks, V, Vs, table, L, B, scale, fmt):
-    """Attention over the whole cache in 64 bits: ``(O, sum p |v| / l, W, e)`` of every head."""
+    """Attention over the whole cache in 64 bits: ``(O, sum p |v| / l, W, e, sum p |v| / l of the p
+    that fp32 may flush)`` of every head."""
     q, Kv, Vv = _np(q), O.q8_values(_np(K), _np(Ks)), O.q8_values(_np(V), _np(Vs))
     vs = _np(Vs)
     n, Hq, d = q.shape
     G = Hq // K.shape[1]
-    out, mag = np.zeros_like(q), np.zeros_like(q)
+    out, mag, low = np.zeros_like(q), np.zeros_like(q), np.zeros_like(q)
     W, e = np.zeros((n, Hq, 1)), np.zeros((n, Hq, 1))
     for b in range(n):
         pos = np.arange(L[b])
@@ -53,20 +57,22 @@ def _reference(q, K, Ks, V, Vs, table, L, B, scale, fmt):
                 p = np.exp(x - x.max())
                 l = p.sum()
                 out[b, h], mag[b, h] = p @ v / l, p @ np.abs(v) / l
+                low[b, h] = (p * (p < 2.0 ** -125)) @ np.abs(v) / l
                 W[b, h] = (p * vs[page, g]).max() * O.QMAX[fmt] / l
                 e[b, h] = scale * (np.abs(k) @ np.abs(q[b, h])).max() * (d / 16 + 4) * 2.0 ** -23
-    return out, mag, W, e
+    return out, mag, W, e, low
 
 
 def _check(got, ref, dtype, keys):
     """``keys``: the most that a warp holds together."""
-    out, mag, W, e = ref
-    tol = mag * (2 * e + 2.0 ** -19) + keys * FLOOR * W
+    out, mag, W, e, low = ref
+    tol = mag * (2 * e + 2.0 ** -19) + keys * FLOOR * W + low
     if dtype == "bf16":
-        tol = tol * (1 + 2.0 ** -8) + 2.0 ** -8 * np.abs(out)
+        tol = tol * (1 + 2.0 ** -8) + np.maximum(2.0 ** -8 * np.abs(out), 2.0 ** -134)
     err = np.abs(_np(got) - out)
-    worst = np.unravel_index(np.argmax(err / tol), err.shape)
-    assert np.all(err <= tol), (worst, _np(got)[worst], out[worst], tol[worst])
+    bad = np.argwhere(~(err <= tol))
+    assert len(bad) == 0, [(len(bad), i.tolist(), _np(got)[tuple(i)], out[tuple(i)], tol[tuple(i)])
+                           for i in bad[:3]]
 
 
 @pytest.mark.parametrize("fmt", ["e4m3", "i8"])
@@ -92,3 +98,82 @@ def test_probabilities_are_held_to_22_bits(ssa, fmt, dtype, d, n):
                                      _dev(table), _dev(np.array(L)), B, 1 << 20)
     ref = _reference(q, K, Ks, V, Vs, table, L, B, 1 / math.sqrt(d), fmt)
     _check(got, ref, dtype, keys=B)
+
+
+def _pool(fmt, exps, logits, B, Hkv, d, seed):
+    """One page for each V exponent (None: all zeros, the least scale) and its logit (log2)."""
+    g = torch.Generator().manual_seed(seed)
+    n = len(exps)
+    K = torch.randint(-7, 8, (n, Hkv, B, d), generator=g).float()
+    V = torch.randn(n, Hkv, B, d, generator=g)
+    V = (V * O.QMAX[fmt] / V.abs().amax(dim=(2, 3), keepdim=True))
+    for i, x in enumerate(exps):
+        if x is None:
+            V[i] = 0
+    V = V.round().to(TORCH[fmt]) if fmt == "i8" else V.to(TORCH[fmt])
+    Vs = torch.tensor([2.0 ** (-126 if x is None else x) for x in exps])[:, None].expand(n, Hkv)
+    Ks = torch.full((n, Hkv), 2.0 ** -5)
+    if logits is not None:  # coordinate 0 alone, so that a q of ln 2 there gives the logit
+        K.zero_()
+        K[..., 0] = torch.tensor(logits, dtype=torch.float32)[:, None, None]
+        Ks = torch.ones(n, Hkv)
+    return K.to(TORCH[fmt]), Ks.contiguous(), V, Vs.float().contiguous()
+
+
+def _decode(ssa, q, K, Ks, V, Vs, table, L, B, **kw):
+    return ssa.ssa_decode_paged_q8(q.to(DEV), K.to(DEV), Ks.to(DEV), V.to(DEV), Vs.to(DEV), None,
+                                   _dev(table), _dev(np.array(L)), B, 1 << 20, **kw)[0]
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "i8"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n,Hkv,G", [(6, 1, 4), (64, 4, 2)])
+def test_values_of_unlike_scales(ssa, fmt, dtype, d, n, Hkv, G):
+    # V scales from 2^-40 to 2^40 and pages of zeros, rising, falling, shuffled and drawn from some
+    # of them, and K scales over three octaves: a row is a block's (6 rows: 8 slices a warp) or is
+    # split between warps and blocks (64 rows of 4 heads: some 13 slices a warp)
+    B, mb = 16, 90
+    exps = [-40, -10, 0, 10, 40, None, 1, 2, 3, -3, -41, 41]
+    K, Ks, V, Vs = _pool(fmt, exps, None, B, Hkv, d, seed=d + n)
+    g = torch.Generator().manual_seed(n)
+    Ks = Ks * torch.exp2(torch.randint(0, 4, Ks.shape, generator=g).float())
+    q = (torch.randn(n, Hkv * G, d, generator=g) * 0.5).to(TORCH[dtype])
+    order = np.argsort([-126 if x is None else x for x in exps])
+    table = np.zeros((n, mb), int)
+    for b in range(n):
+        r = np.random.default_rng(b)
+        some = r.choice(len(exps), size=2 + b % 5, replace=False) if b % 6 > 2 else np.arange(12)
+        rank = np.isin(order, some)
+        row = np.sort(r.integers(0, rank.sum(), mb))
+        row = row[::-1] if b % 3 == 1 else r.permutation(row) if b % 3 == 2 else row
+        table[b] = order[rank][row]
+    L = [mb * B - 7 * (b % 4) for b in range(n)]
+    got = _decode(ssa, q, K, Ks, V, Vs, table, L, B)
+    _check(got, _reference(q, K, Ks, V, Vs, table, L, B, 1 / math.sqrt(d), fmt), dtype, keys=14 * B)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "i8"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("exps,logits", [
+    ([0, -59, -118], [0, 0, 0]), ([0, -40, -80, -119], [0, 0, 0, 0]), ([-118, -59, 0], [0, 0, 0]),
+    ([0, -61], [0, 104]), ([-61, 0], [0, -104]), ([0, 60], [0, -40]), ([60, 0], [0, 104]),
+    ([100, -100], [0, 0]), ([0, 100], [0, -112]), ([100, 0, -100], [-112, -56, 0]),
+    ([None, 20, None, 0], [0, -120, 24, -104]), ([None, 100], [0, -120]), ([None], [0])])
+def test_one_warp_meets_values_of_scales_far_apart(ssa, fmt, dtype, exps, logits):
+    # 96 pages to 12 warps, each in turn: what a warp has summed under one scale must neither
+    # leave fp32's range nor hide what weighs more under another
+    B, d, mb = 16, 64, 96
+    K, Ks, V, Vs = _pool(fmt, exps, logits, B, 1, d, seed=len(exps))
+    q = torch.zeros(1, 4, d)
+    q[..., 0] = math.log(2)
+    q[..., 1:] = torch.randn(1, 4, d - 1, generator=torch.Generator().manual_seed(1)) / 8
+    q = q.to(TORCH[dtype])
+    ways = [[min(i % 8, len(exps) - 1) for i in range(mb)],   # in order, then the last one
+            [max(i % 8 - 8 + len(exps), 0) for i in range(mb)],  # the first one, then in order
+            [i % len(exps) for i in range(mb)]]
+    for way in ways:
+        table = np.array([way])
+        got = _decode(ssa, q, K, Ks, V, Vs, table, [mb * B], B, scale=1.0)
+        ref = _reference(q, K, Ks, V, Vs, table, [mb * B], B, 1.0, fmt)
+        _check(got, ref, dtype, keys=8 * B)
