@@ -40,6 +40,7 @@
 // neither K nor V reads have bank conflicts.  P^T is the S^T tile transposed (movmatrix).
 #include "common.cuh"
 #include "kernels.h"
+#include "ptx.cuh"
 #include "q8.cuh"
 #include "select_block.cuh"
 
@@ -53,6 +54,7 @@ constexpr int kSlice = 16;              // keys a slice
 constexpr int kWholeSlices = 96;        // most slices of a pair that a block takes whole,
 constexpr size_t kWholePairs = 148;     // and most pairs then
 constexpr int kQGridMax = 160;          // most blocks of the split grid (148 SMs, one each)
+constexpr int kTogether = 32;           // most slices whose sums are formed in registers alone
 // Slices in flight or in use a warp: 144 KB (d = 128) or 192 KB (d = 64) a block.
 __host__ __device__ constexpr int q8_stages(int d) { return d == 128 ? 3 : 8; }
 
@@ -453,9 +455,11 @@ __global__ void __launch_bounds__(kQThreads, 1) q8_split_kernel(
   // P is p vs f in f16, vs the scale of V and f a power of two of each head that has the
   // largest weight p vs met so far at 2^kUp or below 2^(kUp + 1).  m (log2) and f change when p
   // passes 2^kLazy or vs f passes kMost, so P stays within 2^15.
-  constexpr float kLazy = 8.0f, kMost = 128.0f;
-  constexpr int kUp = 4;
-  static_assert(kMost * 256.0f <= 32768.0f, "kMost 2^kLazy is within f16");
+  // Half of f16's last bit, 2^-25, is 2^-34 of the largest weight so: 16 K keys just below that
+  // are 2^-20 together.  (kLazy = 8 and kUp = 4 leave 2^-29, and 2^-15.)
+  constexpr float kLazy = 4.0f, kMost = 2048.0f;
+  constexpr int kUp = 9;
+  static_assert(kMost * 16.0f <= 32768.0f, "kMost 2^kLazy is within f16");
   constexpr int stages = q8_stages(D);
   static_assert(stages * 2 * TILE >= REC * 4, "a warp's ring holds its record");
   // the last block's room for two pairs: each m and l of all records, the threads' sums
@@ -480,6 +484,7 @@ __global__ void __launch_bounds__(kQThreads, 1) q8_split_kernel(
   __shared__ int s_split[2], s_first[2], s_parts[2];  // split pairs, their blocks
   __shared__ int s_last[2];                           // those that this block joins
   __shared__ int32_t s_off[kQThreads + 1];
+  __shared__ uint32_t s_tmem;
 
   const int G = Hq / Hkv, spb = B / kSlice;
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
@@ -551,6 +556,20 @@ __global__ void __launch_bounds__(kQThreads, 1) q8_split_kernel(
   float* rec0 = reinterpret_cast<float*>(q8_smem + (size_t)kQW * stages * 2 * TILE);  // [kQW][REC]
   float4* minfo = reinterpret_cast<float4*>(rec0 + kQW * REC) + warp * 8;  // [kQW][8]: rows, ks, vs
 
+  // Sums of more than kTogether slices.  A tile's product is added to its accumulator with the
+  // bits below that one's last cut off: one long sum loses a tail of small weights behind a
+  // large one, and drifts down by up to a step a product (1 K slices, 16 K keys, of weights of
+  // any size: 3e-4 of the result).  So after kTogether slices a warp adds what it has to its
+  // sums in tensor memory and begins anew; nobody else wants that memory here, while the
+  // registers and shared memory are full.  128K keys whole: 53.5 -> 54.1 us (with loads of 8
+  // columns instead of 16 the fp32 form takes 0.4 us more).
+  constexpr int kCols = OT * 4 + 8;  // of a warp: O, then l, m and f of two heads
+  static_assert(kQW / 4 * kCols <= 128, "three warps share a quarter of the lanes");
+  const bool tmem = ns > kQW * kTogether;
+  if (tmem && warp == 0) {
+    ptx::tmem_alloc(&s_tmem, 128);
+    ptx::tmem_relinquish();
+  }
   // the sequence of the block's first slice
   if (t < kQW * 2) s_pair[t >> 1][t & 1] = -1;
   for (int b0 = 0; b0 < batch; b0 += kQThreads) {
@@ -558,8 +577,11 @@ __global__ void __launch_bounds__(kQThreads, 1) q8_split_kernel(
     if (b < batch && (long long)off[b] * Hkv <= s0 && (long long)off[b + 1] * Hkv > s0)
       s_b = b;
   }
+  ptx::tc_fence_before();
   __syncthreads();
+  ptx::tc_fence_after();
   const int b_first = s_b;
+  const uint32_t sums_at = tmem ? s_tmem + ((uint32_t)(warp & 3) << 21) + (warp >> 2) * kCols : 0u;
   if (lists) grid_wait();
 
   // What a slice is: page * Hkv + g (or -1: no keys), first row | rows << 8.
@@ -724,7 +746,52 @@ __global__ void __launch_bounds__(kQThreads, 1) q8_split_kernel(
 #pragma unroll
     for (int i = 0; i < OT; ++i) oc[i][0] = oc[i][1] = oc[i][2] = oc[i][3] = 0.f;
 
-    for (; n < stop; ++n) {
+    bool held = false;  // tensor memory has sums of this pair
+    // Adds them to the present ones, or (keep) these to them, under the present m and f.
+    auto together = [&](bool keep) {
+      float s[8], r[2] = {0.f, 0.f};
+      if (held) {
+        ptx::tmem_ld8(sums_at + OT * 4, s);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float a = s[2 + e] == m_run[e] ? 1.f : ex2(s[2 + e] - m_run[e]);
+          l_run[e] = fmaf(s[e], a, l_run[e]);
+          r[e] = a * f[e] * __uint_as_float(0x7f000000u - __float_as_uint(s[4 + e]));
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < OT; i += 4) {
+        if (held) {
+          float o[16];
+          ptx::tmem_ld16(sums_at + 4 * i, o);
+#pragma unroll
+          for (int c = 0; c < 16; ++c) oc[i + c / 4][c & 3] = fmaf(o[c], r[c & 1], oc[i + c / 4][c & 3]);
+        }
+        if (keep) {
+#pragma unroll
+          for (int j = i; j < i + 4; j += 2) {
+            const float o[8] = {oc[j][0], oc[j][1], oc[j][2], oc[j][3],
+                                oc[j + 1][0], oc[j + 1][1], oc[j + 1][2], oc[j + 1][3]};
+            ptx::tmem_st8(sums_at + 4 * j, o);
+          }
+#pragma unroll
+          for (int c = 0; c < 16; ++c) oc[i + c / 4][c & 3] = 0.f;
+        }
+      }
+      if (keep) {
+        const float z[8] = {l_run[0], l_run[1], m_run[0], m_run[1], f[0], f[1], 0.f, 0.f};
+        ptx::tmem_st8(sums_at + OT * 4, z);
+        ptx::tmem_wait_st();
+        l_run[0] = l_run[1] = 0.f;
+      }
+      held = keep;
+    };
+    for (int upto = min(n + kTogether, stop);; ++n) {
+      if (n == upto) {
+        if (held || n < stop) together(n < stop);
+        if (n == stop) break;
+        upto = min(n + kTogether, stop);
+      }
       issue(n + stages - 1, st == 0 ? stages - 1 : st - 1);
       asm volatile("cp.async.wait_group %0;" ::"n"(stages - 1) : "memory");
       __syncwarp();
@@ -902,7 +969,12 @@ __global__ void __launch_bounds__(kQThreads, 1) q8_split_kernel(
       }
     }
   }
+  ptx::tc_fence_before();
   __syncthreads();
+  if (tmem && warp == 0) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(s_tmem, 128);
+  }
 
   // ---- join the warps' records, pair by pair.  Record 2 w is warp w's first, 2 w + 1
   // its last; those of a pair follow one another.

@@ -496,11 +496,14 @@ ssa_status ssa_append_paged_q8(void* Kp, float* Ks, void* Vp, float* Vs, ssa_qfo
  * One decode step over the 8-bit paged cache: ssa_decode_paged with K and V the
  * values that the codes stand for.  q, O: [batch, Hq, d] of `dtype`.  Sums and
  * softmax are in fp32.  On the tensor cores a weight (p times the block's scale of V) is the
- * sum of two f16: 22 bits, and to 2^-29 of the head's largest weight; q in fp32 is one too,
+ * sum of two f16: 22 bits, and to 2^-34 of the head's largest weight; q in fp32 is one too,
  * relative to each head's largest coordinate; q in bf16 is exact but for coordinates below
- * 2^-12 of the head's largest, which are held to 2^-20 of it.  A p below 2^-126 of the largest
- * is 0.  Scales of V may differ by any factor; the sum of weights times codes has to stay
- * within fp32's range.
+ * 2^-12 of the head's largest, which are held to 2^-20 of it.  The tensor cores sum weights
+ * times codes over 512 keys at most, and fp32 additions do the rest: a result is within 2^-17
+ * of the sum of p |v|, beside what the errors of the logits make, for calls of up to 2^26
+ * attended keys (of all KV heads) (beyond, the error of those additions grows).  A p below 2^-126 of
+ * the largest is 0.  Scales of V may differ by any factor; the sum of weights times codes has
+ * to stay within fp32's range.
  *
  * A sequence with at most topk candidate blocks attends its whole cache and its
  * summaries are not read; S may be NULL when topk >= max_blocks - 2, which is

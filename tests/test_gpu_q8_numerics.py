@@ -15,7 +15,10 @@ With p_t = exp(x_t - max x), l = sum p, and a row's largest weight W = max_t p_t
 - a bf16 result is rounded by half a step, 2^-8 of itself at most, or 2^-134 where it is
   subnormal.
 
-P's last bit: ``FLOOR`` of W for each key, the keys being those that a warp holds together.
+P's last bit: ``FLOOR`` of W for each key, the keys being those that a warp holds together.  Long
+runs: sums of 32 slices, 64 products, each of which cuts off less than a step, 2^-23, of a sum that
+grows evenly (half of 64 2^-23), 2^7 of those sums added with half a step each (2^-24 of a
+growing sum, 2^-18) and the joins (2^-20): 2^-17 of sum p |v| / l.
 """
 import math
 
@@ -28,7 +31,7 @@ from test_gpu_q8 import DEV, TORCH, _dev, _np
 
 pytestmark = [pytest.mark.gpu,
               pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a CUDA device")]
-FLOOR = 2.0 ** -29
+FLOOR = 2.0 ** -34  # half of f16's last bit, 2^-24, where the largest weight is at least 2^9
 
 
 @pytest.fixture(scope="module")
@@ -177,3 +180,77 @@ def test_one_warp_meets_values_of_scales_far_apart(ssa, fmt, dtype, exps, logits
         got = _decode(ssa, q, K, Ks, V, Vs, table, [mb * B], B, scale=1.0)
         ref = _reference(q, K, Ks, V, Vs, table, [mb * B], B, 1.0, fmt)
         _check(got, ref, dtype, keys=8 * B)
+
+
+def _reference_of_pages(q, K, Ks, V, Vs, counts, scale, fmt):
+    """As _reference for one KV head and rows that hold page i ``counts[i]`` times, whole; a key's
+    e is its own here, and in place of it comes what it moves: sum p 2 e |v - O| / l."""
+    q = _np(q)
+    k = O.q8_values(_np(K), _np(Ks))[:, 0]
+    v = O.q8_values(_np(V), _np(Vs))[:, 0]
+    c = np.repeat(np.asarray(counts, float), k.shape[1])
+    vs = np.repeat(_np(Vs)[:, 0], k.shape[1])
+    k, v = k.reshape(-1, k.shape[-1]), v.reshape(-1, v.shape[-1])
+    out, mag, move, W = [], [], [], []
+    for h in range(q.shape[0]):
+        x = scale * (k @ q[h])
+        p = np.exp(x - x[c > 0].max()) * (c > 0)
+        l = (c * p).sum()
+        e = scale * (np.abs(k) @ np.abs(q[h])) * (q.shape[-1] / 16 + 4) * 2.0 ** -23
+        out.append((c * p) @ v / l)
+        mag.append((c * p) @ np.abs(v) / l)
+        move.append((c * p * 2 * e) @ np.abs(v - out[-1]) / l)
+        W.append([(p * vs).max() * O.QMAX[fmt] / l])
+    return np.stack(out), np.stack(mag), np.array(W), np.stack(move)
+
+
+ROWS, BLOCKS = 14, 16384  # 2^21 keys a row; 1034 slices, 16.6 K keys, a warp
+KEYS = 16 * (ROWS * BLOCKS * 128 // 16 // (148 * 12) + 1)
+
+
+def _check_long(got, ref):
+    out, mag, W, move = ref
+    tol = mag * 2.0 ** -17 + move + KEYS * FLOOR * W
+    for row in _np(got):
+        assert np.all(np.abs(row - out) <= tol), (np.abs(row - out) / tol).max()
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "i8"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("tail", [24.7, 27.3, 30.4])
+def test_a_long_tail_behind_one_key(ssa, fmt, d, tail):
+    # key 0 of every row, and 2^21 - 1 keys of 2^-tail of its p each whose V agree; half of the
+    # coordinates of key 0 are 0, so that the tail alone shows there
+    B = 128
+    K = torch.zeros(2, 1, B, d)
+    K[:, 0, :, 0] = -16
+    K[0, 0, 0, 0] = 0
+    V = torch.full((2, 1, B, d), 112.0)
+    V[0, 0, 0, : d // 2] = 0
+    K, V = K.to(TORCH[fmt]), V.to(TORCH[fmt])
+    Ks, Vs = torch.ones(2, 1), torch.full((2, 1), 0.25)
+    q = torch.zeros(ROWS, 2, d)
+    q[..., 0] = tail * math.log(2) / 16
+    table = np.ones((ROWS, BLOCKS))
+    table[:, 0] = 0
+    got = _decode(ssa, q, K, Ks, V, Vs, table, [BLOCKS * B] * ROWS, B, scale=1.0)
+    _check_long(got, _reference_of_pages(q[0], K, Ks, V, Vs, [1, BLOCKS - 1], 1.0, fmt))
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "i8"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("loud", [0.2, 2.0])
+def test_long_runs_of_drawn_keys(ssa, fmt, d, loud):
+    # V of one sign, so that sums grow; even logits, and ones that a few keys carry
+    B, pages = 128, 64
+    g = torch.Generator().manual_seed(d)
+    K = torch.randint(-7, 8, (pages, 1, B, d), generator=g).to(TORCH[fmt])
+    V = torch.randint(40, 128, (pages, 1, B, d), generator=g).float().to(TORCH[fmt])
+    Ks, Vs = torch.full((pages, 1), 0.25), torch.exp2(torch.randint(-6, -3, (pages, 1), generator=g))
+    q = (torch.randn(1, 2, d, generator=g) * loud).expand(ROWS, 2, d).contiguous()
+    row = torch.randint(0, pages, (BLOCKS,), generator=g).numpy()
+    table = np.stack([np.random.default_rng(b).permutation(row) for b in range(ROWS)])
+    got = _decode(ssa, q, K, Ks, V, Vs.float(), table, [BLOCKS * B] * ROWS, B)
+    ref = _reference_of_pages(q[0], K, Ks, V, Vs.float(), np.bincount(row, minlength=pages),
+                              1 / math.sqrt(d), fmt)
+    _check_long(got, ref)
