@@ -503,7 +503,7 @@ ssa_status ssa_decode_paged_q8(const void* q, ssa_dtype dtype, const void* Kp, c
   if (st != SSA_OK) return st;
   if (batch <= 0 || Hq <= 0 || topk < 0 || Hq % Hkv != 0) return SSA_ERR_INVALID_ARG;
   if (Hq / Hkv > 8) return SSA_ERR_UNSUPPORTED;
-  if (max_blocks > 16384) return SSA_ERR_UNSUPPORTED;
+  if (max_blocks > ssa::kQ8MaxBlocks) return SSA_ERR_UNSUPPORTED;
   // the 16-key slices of the whole batch are counted in 32 bits
   if ((long long)batch * max_blocks * (B / 16) > 0x7fffffffLL ||
       (long long)batch * Hkv > 0x7ffffffeLL)

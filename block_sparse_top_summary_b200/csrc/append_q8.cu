@@ -335,7 +335,7 @@ static cudaError_t launch_append_q8_t(void* Kp, float* Ks, void* Vp, float* Vs, 
                                       long long tok_stride, long long head_stride, int batch,
                                       int T_max, int Hkv, int B, int max_blocks, int num_pages,
                                       cudaStream_t st) {
-  const int chunks = sizeof(T) == 2 ? 8 : 4;
+  constexpr int chunks = sizeof(T) == 2 ? 8 : 4;
   const int threads = (B * (D / 8) / chunks + 31) / 32 * 32;  // 32 .. 512
   const long long units = T_max / B + 2LL * batch;
   // All heads of a unit in one block where the units alone fill the GPU (2 blocks for
@@ -351,10 +351,13 @@ static cudaError_t launch_append_q8_t(void* Kp, float* Ks, void* Vp, float* Vs, 
   if (heads == Hkv && Hkv >= 7 && 2 * blocks * threads < 3LL * 148 * 512) heads = (Hkv + 1) / 2;
   const dim3 grid((unsigned)units, (unsigned)(2 * ((Hkv + heads - 1) / heads)));
   // two heads' rows (16 KB each for 64 rows of 128 in bf16), and the threads' sums
-  const int smem = threads * (2 * chunks * 8 * (int)sizeof(T) + 8 * (int)sizeof(float));
+  constexpr int each = 2 * chunks * 8 * (int)sizeof(T) + 8 * (int)sizeof(float);
+  const int smem = threads * each;
   if (smem > 47 * 1024) {  // the static array counts too
-    const cudaError_t e = cudaFuncSetAttribute(
-        append_q8_kernel<T, D, F>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    // (the limit is the kernel's, for all host threads: always that of B = 128)
+    const cudaError_t e =
+        cudaFuncSetAttribute(append_q8_kernel<T, D, F>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             128 * (D / 8) / chunks * each);
     if (e != cudaSuccess) return e;
   }
   cudaLaunchAttribute attr{};

@@ -1225,10 +1225,12 @@ static cudaError_t launch_q8_t(const Q8Plan& p, const void* q, const void* Kp, c
   // the GPU takes at once (2 an SM) and as leave each warp two steps of 16.
   int CS = 1;
   while (CS < 8 && batch * (long long)Hkv * CS * 2 <= 2 * sms && max_blocks >= CS * 2 * 256) CS *= 2;
-  const size_t smem1 = sizeof(float) * (D + 512 + kListCap + kListCap / 2 + (size_t)max_blocks);
+  constexpr size_t fixed = D + 512 + kListCap + kListCap / 2;
+  const size_t smem1 = sizeof(float) * (fixed + (size_t)max_blocks);
   if (smem1 > 47 * 1024) {  // the static arrays count too
+    // (the limit is the kernel's, for all host threads: always that of the longest table)
     e = cudaFuncSetAttribute(q8_route_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)smem1);
+                             (int)(sizeof(float) * (fixed + kQ8MaxBlocks)));
     if (e != cudaSuccess) return e;
   }
   attr[1].id = cudaLaunchAttributeClusterDimension;

@@ -129,6 +129,8 @@ cudaError_t launch_append_q8(void* Kp, float* Ks, void* Vp, float* Vs, ssa_qform
                              long long head_stride, int batch, int T_max, int Hkv, int d, int B,
                              int max_blocks, int num_pages, cudaStream_t st);
 
+constexpr int kQ8MaxBlocks = 16384;  // blocks of a sequence, at most
+
 struct Q8Plan {
   int kk;      // effective top-k: min(topk, max_blocks)
   int width;   // idx row width: kk + 2

@@ -419,8 +419,9 @@ cudaError_t launch_page_plan(const int32_t* have, const int32_t* want, const int
   const bool one = max_new <= 8 * kPlanThreads;
   const auto kernel = one ? page_plan_kernel<true> : page_plan_kernel<false>;
   if (smem > 46 * 1024) {  // the static arrays count too
-    const cudaError_t e =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    // (the limit is the kernel's, for all host threads: always that of the largest batch)
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               kPlanMaxBatch * 6 * (int)sizeof(int));
     if (e != cudaSuccess) return e;
   }
   cudaLaunchAttribute attr[2] = {};

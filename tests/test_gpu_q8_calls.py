@@ -1,0 +1,108 @@
+"""Calls of the page plan and the 8-bit cache that a program makes and single calls do not show:
+from several host threads at once, and with strides that mean nothing."""
+import threading
+
+import numpy as np
+import pytest
+import torch
+
+from test_gpu_q8 import DEV, _dev
+
+pytestmark = [pytest.mark.gpu,
+              pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a CUDA device")]
+
+
+@pytest.fixture(scope="module")
+def ssa():
+    import block_sparse_top_summary_b200 as m
+    m.load_library()
+    return m
+
+
+def _plans(ssa, batch, stream):
+    """One-token plans of ``batch`` rows (24 bytes of shared memory a row)."""
+    have = _dev(np.arange(batch) % 40)
+    table = torch.arange(batch * 4, dtype=torch.int32, device=DEV).view(batch, 4)
+    ring, pool = _dev(np.arange(batch) + 4 * batch), _dev(np.array([0, batch]))
+    out = [torch.empty(x, dtype=torch.int32, device=DEV) for x in (batch, batch + 1, batch, 2)]
+    return table, *ssa.ssa_page_plan(have, have + 1, table, ring, pool, 16, batch, got=out[0],
+                                     cu=out[1], slots=out[2], pool_out=out[3],
+                                     stream=stream), have, ring, pool
+
+
+def _appends(ssa, B, stream):
+    """Whole blocks of B rows (576 bytes of shared memory a row in bf16)."""
+    d, n = 128, 4
+    K, V = (torch.zeros(n, 1, B, d, dtype=torch.int8, device=DEV) for _ in range(2))
+    Ks, Vs = (torch.zeros(n, 1, device=DEV) for _ in range(2))
+    S = torch.zeros(n, 1, 1, d, device=DEV)
+    k = torch.randn(n * B, 1, d, device=DEV).bfloat16()
+    new = _dev(np.arange(n * B)), _dev(np.arange(n + 1) * B), _dev(np.full(n, B)), k
+    ssa.ssa_append_paged_q8(K, Ks, V, Vs, S, *new, k, B, stream=stream)
+    return K, Ks, V, Vs, S, *new
+
+
+def _decodes(ssa, max_blocks, stream):
+    """Routed rows under a table of ``max_blocks`` (4 bytes of shared memory a block)."""
+    B, d = 16, 64
+    g = torch.Generator().manual_seed(max_blocks)
+    K, V = (torch.randint(-127, 128, (50, 1, B, d), generator=g).to(DEV, torch.int8)
+            for _ in range(2))
+    Ks, Vs = (torch.full((50, 1), 2.0 ** -6, device=DEV) for _ in range(2))
+    S = torch.randn(1, 1, max_blocks, d, generator=g).to(DEV)
+    table = torch.randint(0, 50, (1, max_blocks), generator=g).to(DEV, torch.int32)
+    q, lens = torch.randn(1, 4, d, generator=g).to(DEV), _dev(np.array([16 * 600]))
+    ws = torch.empty(ssa.ssa_decode_paged_q8_workspace_size(1, 4, 1, d, B, 8, max_blocks),
+                     dtype=torch.uint8, device=DEV)
+    O, idx = torch.empty_like(q), torch.empty(1, 1, 10, dtype=torch.int32, device=DEV)
+    ssa.ssa_decode_paged_q8(q, K, Ks, V, Vs, S, table, lens, B, 8, O=O, idx=idx, workspace=ws,
+                            stream=stream)
+    return O, idx, K, V, Ks, Vs, S, table, q, lens, ws
+
+
+class _Recorder:
+    """The library, with the packed arguments of each call kept."""
+    def __init__(self, lib):
+        self.lib, self.calls = lib, []
+
+    def __getattr__(self, name):
+        fn = getattr(self.lib, name)
+        if not name.endswith("_words"):
+            return fn
+
+        def call(words):
+            self.calls.append((fn, words))
+            return fn(words)
+        return call
+
+
+@pytest.mark.parametrize("make,sizes", [(_plans, (2100, 8192, 4000)), (_appends, (96, 128, 112)),
+                                        (_decodes, (11500, 16384, 13000))])
+def test_host_threads_with_calls_of_other_sizes(ssa, monkeypatch, make, sizes):
+    # each thread's calls need another amount of shared memory of one kernel; the calls can be
+    # repeated on their buffers, and are made without the binding's own work between them
+    rec = _Recorder(ssa.load_library())
+    monkeypatch.setattr("block_sparse_top_summary_b200.abi.load_library", lambda: rec)
+    streams = [torch.cuda.Stream() for _ in sizes]
+    torch.cuda.synchronize()
+    tensors = []
+    for x, s in zip(sizes, streams):
+        with torch.cuda.stream(s):  # (so that the inputs are ready when the call runs)
+            tensors.append(make(ssa, x, s))
+    torch.cuda.synchronize()
+    want = [[t.clone() for t in ts] for ts in tensors]
+    start, bad = threading.Barrier(len(sizes)), []
+
+    def work(fn, words):
+        start.wait()
+        bad.extend(st for st in (fn(words) for _ in range(20000)) if st != 0)
+
+    threads = [threading.Thread(target=work, args=c) for c in rec.calls]
+    assert len(threads) == len(sizes)
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert bad == []
+    assert all(torch.equal(a, b) for ts, ref in zip(tensors, want) for a, b in zip(ts, ref))
