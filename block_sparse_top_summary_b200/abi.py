@@ -512,11 +512,23 @@ def ssa_sparse_attn_bwd(Q, K, V, O, dO, lse, idx, cnt, B: int, scale: float | No
 # fails), the current device and stream are read without building torch's
 # Python objects for them, and the arguments go in one packed array (24 ctypes
 # arguments cost 3 us, the array 0.8).
-_device = torch._C._cuda_getDevice
-_current_stream = torch._C._cuda_getCurrentRawStream
+# Where torch lacks those two short ways, its public ones serve.
+_get_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_current_stream = (getattr(torch._C, "_cuda_getCurrentRawStream", None)
+                   or (lambda dev: torch.cuda.current_stream(dev).cuda_stream))
 _plan_words = struct.Struct("=16q").pack
 _append_words = struct.Struct("=22q").pack
 _decode_words = struct.Struct("=18qd5q").pack
+
+
+def _device() -> int:
+    """The current device; -2, on which no tensor is, where there is none."""
+    try:
+        return _get_device()
+    except (RuntimeError, AssertionError):  # no driver; a torch without CUDA
+        if torch.cuda.is_available():
+            raise
+        return -2
 
 
 def _refuse(dev: int, *args):
