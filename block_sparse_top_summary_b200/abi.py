@@ -667,10 +667,14 @@ def ssa_append_paged_q8(Kp, Ks, Vp, Vs, S, slots, cu, seqlens, k_new, v_new, B: 
             or not (slots.is_contiguous() and cu.is_contiguous() and seqlens.is_contiguous())):
         _refuse(dev, ("slots", slots, i32, (T,)), ("cu", cu, i32, (batch + 1,)),
                 ("seqlens", seqlens, i32, (batch,)))
-    strides, new = k_new.stride(), (T, Hkv, d)
+    strides, v_strides, new = k_new.stride(), v_new.stride(), (T, Hkv, d)
+    if k_new.shape == v_new.shape == new and (T <= 1 or Hkv == 1):
+        # what a dimension of one steps by does not matter: as if contiguous
+        strides, v_strides = ((s[0] if T > 1 else Hkv * d, s[1] if Hkv > 1 else d, s[2])
+                              for s in (strides, v_strides))
     if (k_new.shape != new or v_new.shape != new or k_new.dtype is not v_new.dtype
             or k_new.get_device() != dev or v_new.get_device() != dev
-            or v_new.stride() != strides or strides[2] != 1):
+            or v_strides != strides or strides[2] != 1):
         raise ValueError(f"k_new and v_new must be {list(new)} on the current device (cuda:{dev}), "
                          "of one dtype, of equal strides and contiguous in d")
     status = load_library().ssa_append_paged_q8_words(_append_words(

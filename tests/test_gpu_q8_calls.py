@@ -106,3 +106,33 @@ def test_host_threads_with_calls_of_other_sizes(ssa, monkeypatch, make, sizes):
     torch.cuda.synchronize()
     assert bad == []
     assert all(torch.equal(a, b) for ts, ref in zip(tensors, want) for a, b in zip(ts, ref))
+
+
+@pytest.mark.parametrize("T,Hkv", [(1, 2), (21, 1), (1, 1), (0, 2)])
+def test_strides_of_dimensions_of_one_do_not_matter(ssa, T, Hkv):
+    # one token, or one head: k_new and v_new address the same memory whatever that stride is
+    B, d = 16, 64
+    slots, cu, lens = _dev(np.arange(T)), _dev(np.array([0, T])), _dev(np.array([T]))
+    k = torch.randn(T, Hkv, d, device=DEV)
+    wide = torch.randn(T, 3 * Hkv, d, device=DEV)
+    odd = torch.empty_strided((T, Hkv, d), (Hkv * d if T > 1 else 3, d if Hkv > 1 else 7, 1),
+                              device=DEV).copy_(k)
+
+    def run(k, v):
+        K, V = (torch.zeros(3, Hkv, B, d, dtype=torch.int8, device=DEV) for _ in range(2))
+        Ks, Vs = (torch.zeros(3, Hkv, device=DEV) for _ in range(2))
+        S = torch.zeros(1, Hkv, 3, d, device=DEV)
+        return ssa.ssa_append_paged_q8(K, Ks, V, Vs, S, slots, cu, lens, k, v, B)
+
+    same = run(k, k)
+    got = [run(odd, k), run(k, odd), run(odd, odd)]
+    v = wide[:, Hkv:2 * Hkv] if T <= 1 else None  # a slice of a wider row, of one token
+    if v is not None:
+        for a, b in zip(run(k, v.contiguous()), run(k, v)):
+            assert torch.equal(a, b)
+    for out in got:
+        for a, b in zip(same, out):
+            assert torch.equal(a, b)
+    if T > 1:  # a stride that does matter still has to agree
+        with pytest.raises(ValueError):
+            run(k, wide[:, :1])
