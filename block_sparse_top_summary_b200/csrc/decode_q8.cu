@@ -596,8 +596,8 @@ __global__ void __launch_bounds__(kQThreads, 1) q8_split_kernel(
     while ((long long)off[b + 1] * Hkv <= s) ++b;
     const int L = seqlens[b];
     const int per = off[b + 1] - off[b];
-    const int in = (int)(s - (long long)off[b] * Hkv);
-    const int g = in / per, k = in - g * per;
+    const long long in = s - (long long)off[b] * Hkv;  // (all heads' slices pass 32 bits)
+    const int g = quotient(in, per), k = (int)(in - (long long)g * per);
     const int e = k / spb, sub = k - e * spb;
     const int last = (L - 1) / B;
     const int j = last - 1 > kk ? ws_idx[((int64_t)b * Hkv + g) * width + e] : e;

@@ -136,3 +136,27 @@ def test_strides_of_dimensions_of_one_do_not_matter(ssa, T, Hkv):
     if T > 1:  # a stride that does matter still has to agree
         with pytest.raises(ValueError):
             run(k, wide[:, :1])
+
+
+def test_slices_of_all_heads_past_31_bits(ssa):
+    # 16400 heads of 2^21 keys: a sequence's 16-key slices, counted over its heads, pass 2^31.  All
+    # blocks are page 0, so a head's result is the attention over its 128 rows there.
+    B, d, Hkv, mb = 128, 64, 16400, 16384
+    g = torch.Generator(device=DEV).manual_seed(3)
+    K, V = (torch.randint(-127, 128, (1, Hkv, B, d), generator=g, device=DEV, dtype=torch.int8)
+            for _ in range(2))
+    Ks, Vs = (torch.full((1, Hkv), 2.0 ** -6, device=DEV) for _ in range(2))
+    q = torch.randn(1, Hkv, d, generator=g, device=DEV)
+    table = torch.zeros(1, mb, dtype=torch.int32, device=DEV)
+    out, _ = ssa.ssa_decode_paged_q8(q, K, Ks, V, Vs, None, table, _dev(np.array([mb * B])), B,
+                                     1 << 20, want_idx=False)
+    k, v = (x[0].double() * 2.0 ** -6 for x in (K, V))
+    x = (k @ q[0].double()[:, :, None])[..., 0] / 8
+    p = torch.softmax(x, -1)
+    ref = (p[:, None] @ v)[:, 0]
+    mag = (p[:, None] @ v.abs())[:, 0]
+    # as in test_gpu_q8_numerics: a logit is off by e, the sums by 2^-17 of the magnitudes;
+    # 1.2 M slices a warp make 2^15.2 sums of 32 slices, 2^13 a pair: 2^-24 of the growing sum each
+    e = (k.abs() @ q[0].double().abs()[:, :, None]).amax((1, 2)) / 8 * (d / 16 + 4) * 2.0 ** -23
+    tol = mag * (2 * e[:, None] + 2.0 ** -17 + 2.0 ** (13 - 24 - 1))
+    assert ((out[0].double() - ref).abs() <= tol).all()
