@@ -17,14 +17,19 @@
 //
 // Bounds: up to a few thousand slots the launch and the chain of one block (lengths,
 // scan, pages: 6 us for 256 one-token rows); beyond, the instructions that place a
-// slot, which want the whole GPU.  So up to 8192 slots one block does it all, and
-// beyond a cluster of 8 does rows and pages (all of its blocks form the sums, and a
+// slot, which want the whole GPU.  So up to 8192 slots and 4096 rows one block does it all,
+// and beyond a cluster of 8 does rows and pages (all of its blocks form the sums, and a
 // cluster barrier stands before the last writes) and a second kernel the slots.
 // Cluster and slots kernel against one block, us: 256 rows of 1 token 16.4, 6.1; 4000
 // rows of 1 24.3, 14.3; 8 rows of 1000 8.2, 9.1; 64 rows of 250 10.2, 16.4; 4 rows of 8000
 // 10.2, 24.6.  0.47 million slots of 1024 rows with 31 thousand pages: 18 us (16.4 with
 // calls back to back, which overlap; 256 one-token rows then 4.1); with
 // the slots in the cluster 31 us, in one block 637 us.
+// Pages that come back are moved as well, and the host knows nothing of their number: rows of
+// one token, of which some have finished, cluster and slots kernel against one block, us: 256
+// rows, none 14.4, 4.2; 22 K pages back 14.9, 16.7; 1024 rows, 68 K back 27.2, 29.2; 4096
+// rows, none 21.4, 15.9; 23 K back 28.8, 27.4; 246 K back 38.9, 85.7; 8192 rows, none 34.0,
+// 34.5; 335 K back 51.2, 117.  One block keeps the quiet steps, up to where it gains nothing.
 #include "common.cuh"
 #include "kernels.h"
 
@@ -416,7 +421,7 @@ cudaError_t launch_page_plan(const int32_t* have, const int32_t* want, const int
                              int32_t* cu, int32_t* slots, int max_new, cudaStream_t st) {
   const size_t smem = (size_t)batch * 6 * sizeof(int);
   // (the rule's two sides are measured at the top)
-  const bool one = max_new <= 8 * kPlanThreads;
+  const bool one = max_new <= 8 * kPlanThreads && batch <= 4 * kPlanThreads;
   const auto kernel = one ? page_plan_kernel<true> : page_plan_kernel<false>;
   if (smem > 46 * 1024) {  // the static arrays count too
     // (the limit is the kernel's, for all host threads: always that of the largest batch)
@@ -440,7 +445,7 @@ cudaError_t launch_page_plan(const int32_t* have, const int32_t* want, const int
   const cudaError_t e =
       cudaLaunchKernelEx(&cfg, kernel, have, want, keep, batch, B, table, max_blocks, num_pages,
                          ring, pool, pool_out, got, cu, slots, max_new);
-  if (e != cudaSuccess || one) return e;
+  if (e != cudaSuccess || one || max_new == 0) return e;
   cfg.gridDim = dim3((unsigned)((max_new + 2047) / 2048));
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = 0;

@@ -6,7 +6,7 @@ import numpy as np
 import pytest
 import torch
 
-from test_gpu_q8 import DEV, _dev
+from test_gpu_q8 import DEV, _check_plan, _dev, _plan_case
 
 pytestmark = [pytest.mark.gpu,
               pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a CUDA device")]
@@ -160,3 +160,12 @@ def test_slices_of_all_heads_past_31_bits(ssa):
     e = (k.abs() @ q[0].double().abs()[:, :, None]).amax((1, 2)) / 8 * (d / 16 + 4) * 2.0 ** -23
     tol = mag * (2 * e[:, None] + 2.0 ** -17 + 2.0 ** (13 - 24 - 1))
     assert ((out[0].double() - ref).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("n", [4096, 4097, 8192])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_plan_of_many_rows_and_few_tokens(ssa, n, in_place):
+    # on both sides of the rows that one block takes: no slot at all, some, and all that are asked
+    # for; most rows give pages back or are refused
+    for max_new in (0, 1, 300, 8192):
+        _check_plan(ssa, _plan_case(n, 16, 9, seed=n + max_new, prompt=5), 16, max_new, in_place)
