@@ -579,7 +579,8 @@ def ssa_page_plan(have, want, page_table, ring, pool, B: int, max_new: int, keep
     ``[batch, max_blocks]`` and ``ring`` ``[num_pages]`` are changed in place;
     ``pool`` ``[2]``: first free entry of the ring and number of free pages.
     ``keep``: ``[batch]`` leading blocks that are not freed.  ``got=have`` and
-    ``pool_out=pool`` update these in place.
+    ``pool_out=pool`` update these in place.  Results that are not given are views of one
+    allocation: a program that keeps ``got`` and drops ``slots`` gives its own.
     """
     i32, dev = torch.int32, _device()
     batch, max_blocks = page_table.shape

@@ -17,14 +17,20 @@
 //      lies within a warp's run is written at once; the others' records are joined
 //      in shared memory, and a pair that is split between blocks is finished by the
 //      last of them, from the blocks' records in order.  The kernel starts while the
-//      route kernel runs (programmatic dependent launch) and waits only for lists.
+//      route kernel runs (programmatic dependent launch) and waits only for lists, and
+//      before its end.  Until then it reads what the kernels before the call have written and
+//      writes O, idx and records: that is safe because every block of the route kernel lets it in
+//      only behind its own wait for those kernels.  Whatever is launched between the two has
+//      to keep to that.
+// Both rules on row lengths go by the table's width, as the lengths are on the device: a
+// wide table takes the two kernels however short its rows.
 // Measured (B200, calls back to back in a CUDA graph): 128K keys of 8 heads, d = 128, e4m3,
-// read whole (0.27 GB): 53.4 us, of which the blocks' streams take 38 to 46 (24 of the 148 SMs
+// read whole (0.27 GB): 54 us, of which the blocks' streams take 38 to 46 (24 of the 148 SMs
 // are a tenth slower under load), start and joins the rest; 32 ragged rows of up to 16K
-// keys, int8 (0.67 GB): 115 us (5.8 TB/s); 64 rows of 65536 keys, top-32 (0.27 GB of
-// summaries, 0.28 GB of codes): 104.6 us; one row of 128K keys, top-32: 17.9 us.  A first form
-// with a barrier of all warps at every pair's end, the heads as the tiles' rows and a
-// serial join took 74, 175, 138 and 39 us.
+// keys, int8 (0.67 GB): 115 us cool, 127 under a sustained load, which meets the power limit;
+// 64 rows of 65536 keys, top-32 (0.27 GB of summaries, 0.28 GB of codes): 104.8 us; one row of
+// 128K keys, top-32: 18.0 us.  A first form with a barrier of all warps at every pair's end,
+// the heads as the tiles' rows and a serial join took 74, 175, 138 and 39 us.
 //
 // Fragments.  m16n8k16 tiles, f16 in and fp32 out, with the cache as the row operand:
 // S^T = K q^T has a tile's 16 rows for the slice's keys and its 8 columns for the
@@ -469,8 +475,8 @@ __global__ void __launch_bounds__(kQThreads, 1) q8_split_kernel(
   static_assert(kQThreads >= 8 * D / 4 && kJoinStage >= kQThreads, "PS and cap are 1 at least");
   // q against e4m3 codes, or in fp32: f16 against keys turned into f16, with a low part
   // in fp32.  q in bf16 against int8 codes: three int8 digits against the codes
-  // themselves, which saves turning K (with P in two f16, 410 -> 392 instructions a slice;
-  // 32 ragged rows under a sustained load, where int8 meets the power limit, 132 -> 127 us).
+  // themselves, which saves turning K (410 -> 392 instructions a slice; 32 ragged rows under a
+  // sustained load, where int8 meets the power limit, 132 -> 127 us).
   // e4m3 has no such tile: the one that PTX offers here turns its operands into f16 as
   // well (9 to 12 cycles an SM quarter for k = 32 at a latency of 47, f16 8.3 for k = 16 at
   // 24), and was slower (56 -> 65 us for 128K keys).
@@ -582,7 +588,7 @@ __global__ void __launch_bounds__(kQThreads, 1) q8_split_kernel(
   ptx::tc_fence_after();
   const int b_first = s_b;
   const uint32_t sums_at = tmem ? s_tmem + ((uint32_t)(warp & 3) << 21) + (warp >> 2) * kCols : 0u;
-  if (lists) grid_wait();
+  if (lists) grid_wait();  // (else at the end: see the top for what makes that safe)
 
   // What a slice is: page * Hkv + g (or -1: no keys), first row | rows << 8.
   struct Slice {

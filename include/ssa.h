@@ -499,11 +499,11 @@ ssa_status ssa_append_paged_q8(void* Kp, float* Ks, void* Vp, float* Vs, ssa_qfo
  * sum of two f16: 22 bits, and to 2^-34 of the head's largest weight; q in fp32 is one too,
  * relative to each head's largest coordinate; q in bf16 is exact but for coordinates below
  * 2^-12 of the head's largest, which are held to 2^-20 of it.  The tensor cores sum weights
- * times codes over 512 keys at most, and fp32 additions do the rest: a result is within 2^-17
- * of the sum of p |v|, beside what the errors of the logits make, for calls of up to 2^26
- * attended keys (of all KV heads) (beyond, the error of those additions grows).  A p below 2^-126 of
- * the largest is 0.  Scales of V may differ by any factor; the sum of weights times codes has
- * to stay within fp32's range.
+ * times codes over 512 keys at most, and fp32 additions do the rest: beside what the errors of
+ * the logits make, a result is within 2^-17 of the sum of p |v| in calls that attend up to 2^26
+ * keys, counted over the KV heads; beyond, the error of those additions grows.  A p below 2^-126
+ * of the largest is 0.  Scales of V may differ by any factor; the sum of weights times codes
+ * has to stay within fp32's range.
  *
  * A sequence with at most topk candidate blocks attends its whole cache and its
  * summaries are not read; S may be NULL when topk >= max_blocks - 2, which is
@@ -513,9 +513,10 @@ ssa_status ssa_append_paged_q8(void* Kp, float* Ks, void* Vp, float* Vs, ssa_qfo
  * O and idx must not overlap the inputs.
  * workspace: >= ssa_decode_paged_q8_workspace_size(...) bytes, 256-byte aligned,
  * contents on entry ignored; calls that share one must not overlap on the
- * device.  The size is 0, and the workspace may be NULL, for a few short rows
- * read whole.  Hq / Hkv <= 8; max_blocks <= 16384; batch * max_blocks * B / 16 < 2^31
- * and batch * Hkv * (blocks attended by a row, at most) * B / 16 <= 2^37.
+ * device.  The size is 0, and the workspace may be NULL, for a few rows read whole under a
+ * short table (max_blocks decides, not the lengths).  Hq / Hkv <= 8; max_blocks <= 16384;
+ * batch * max_blocks * B / 16 < 2^31 and batch * Hkv * (blocks attended by a row, at most) *
+ * B / 16 <= 2^37.
  */
 ssa_status ssa_decode_paged_q8_workspace_size(int batch, int Hq, int Hkv, int d, int B, int topk,
                                               int max_blocks, size_t* bytes);
