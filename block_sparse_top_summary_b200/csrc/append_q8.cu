@@ -14,7 +14,7 @@
 // of few rows (decode steps) are left to single warps, a head each, without a barrier.
 // 52233 tokens of 8 heads, d = 128, B = 64 (bf16 to e4m3; 0.32 GB): 229 us with one block of
 // 256 threads a tile and a bisection of dependent loads, 54 us (6.0 TB/s) this way, with
-// the arithmetic at some 65% of the issue slots: 8 chunks a thread (4: 69 us) and
+// the arithmetic at some 58% of the issue slots: 8 chunks a thread (4: 69 us) and
 // mixed-precision FMAs on the bf16 elements (unpacked first: 76 us) cut that.  64 single
 // tokens: 17 us before, 3.6 us (calls back to back in a CUDA graph).
 //

@@ -169,3 +169,44 @@ def test_plan_of_many_rows_and_few_tokens(ssa, n, in_place):
     # for; most rows give pages back or are refused
     for max_new in (0, 1, 300, 8192):
         _check_plan(ssa, _plan_case(n, 16, 9, seed=n + max_new, prompt=5), 16, max_new, in_place)
+
+
+def test_long_rows_on_two_streams_and_in_one_graph(ssa):
+    # runs that are summed in tensor memory (over 32 slices a warp), two calls at once
+    B, d, mb = 128, 64, 8192
+    g = torch.Generator().manual_seed(5)
+    K, V = (torch.randint(-127, 128, (20, 1, B, d), generator=g).to(DEV, torch.int8)
+            for _ in range(2))
+    Ks, Vs = (torch.full((20, 1), 2.0 ** -6, device=DEV) for _ in range(2))
+    table = torch.randint(0, 20, (1, mb), generator=g).to(DEV, torch.int32)
+    lens = _dev(np.array([mb * B - 77]))
+    qs = [torch.randn(1, 4, d, generator=g).to(DEV) for _ in range(2)]
+
+    def call(q, **kw):
+        return ssa.ssa_decode_paged_q8(q, K, Ks, V, Vs, None, table, lens, B, 1 << 20,
+                                       want_idx=False, **kw)[0]
+
+    want = [call(q).clone() for q in qs]
+    streams = [torch.cuda.Stream() for _ in qs]
+
+    def both():
+        out = []
+        for q, s in zip(qs, streams):
+            s.wait_stream(torch.cuda.current_stream())
+            out.append(call(q, stream=s))
+        for s in streams:
+            torch.cuda.current_stream().wait_stream(s)
+        return out
+
+    for _ in range(20):
+        for a, b in zip(both(), want):
+            assert torch.equal(a, b)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = both()
+    for _ in range(3):
+        for a in out:
+            a.zero_()
+        graph.replay()
+        for a, b in zip(out, want):
+            assert torch.equal(a, b)
